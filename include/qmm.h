@@ -294,6 +294,191 @@ qmm_status qmm_get_rows_q5_0(const void *w, const int32_t *ids, float *out, int6
 qmm_status qmm_get_rows_q5_1(const void *w, const int32_t *ids, float *out, int64_t n_ids, int64_t N, int64_t K,
                              void *stream);
 
+/* ---- attention: rotary positions, key-value cache, decode attention ----------
+ * Rows here are rows of D values of one token and one head, in f32, f16 or
+ * bf16 (qmm_dtype), the values of a row contiguous and token t, head h at
+ *   data + t * token_stride + h * head_stride     (strides in elements),
+ * so slices of a fused QKV product can be passed as they are.  Pointers to rows
+ * and both strides are multiples of four elements (QMM_E_ALIGN otherwise);
+ * strides are not negative.  Index arrays (positions, slots, pages, lens) and
+ * f32 arrays need the alignment of their type.  T, B, Hq, H >= 1. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
+
+/* Which two values of a row are rotated together, of the first `rot`: value i
+ * with i + rot/2 (HALF), or value 2i with 2i + 1 (INTERLEAVED). */
+typedef enum { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 } qmm_rope_order;
+
+/* A model's rotation: kept by the caller for as long as it is used. */
+typedef struct {
+    const double *freqs; /* f64 [rot/2], device memory: the angle of pair i per position, in radians */
+    int64_t rot;         /* values of a row that are rotated: even, 2 <= rot <= D; the others are copied */
+    int32_t order;       /* qmm_rope_order */
+    float mscale;        /* factor on the cosine and the sine (1, or a long-context method's) */
+} qmm_rope_plan;
+
+/* Frequencies for qmm_rope_plan, on the host.  f_i = base^(-2i/rot), then
+ *   QMM_ROPE_PLAIN      as they are;
+ *   QMM_ROPE_LINEAR     f_i / factor (positions interpolated);
+ *   QMM_ROPE_NTK        with base * factor^(rot/(rot-2)): the slowest frequency
+ *                       is divided by factor, the fastest kept;
+ *   QMM_ROPE_YARN       f_i / factor where a pair turns less than `low` times in
+ *                       trained_len positions, f_i where it turns more than
+ *                       `high` times, a linear ramp over the pair index between
+ *                       (its ends rounded outwards to whole pairs), and
+ *                       mscale = 1 + 0.1 ln(factor);
+ *   QMM_ROPE_BANDS      f_i / factor for wavelengths over trained_len / low, f_i
+ *                       below trained_len / high, between them f_i times
+ *                       (1-s)/factor + s, s = (trained_len/wavelength - low) / (high - low).
+ * factor >= 1; low and high (0 < low < high) and trained_len > 0 are read by
+ * the last two only.
+ *   freqs  : f64 [rot/2], HOST memory, written.
+ *   mscale : HOST, written (1 except for YARN); may be NULL. */
+typedef enum {
+    QMM_ROPE_PLAIN = 0, QMM_ROPE_LINEAR = 1, QMM_ROPE_NTK = 2, QMM_ROPE_YARN = 3, QMM_ROPE_BANDS = 4
+} qmm_rope_scaling;
+qmm_status qmm_rope_freqs(double *freqs, float *mscale, int64_t rot, double base, int scaling, double factor,
+                          double trained_len, double low, double high);
+
+/* Rotary positions: every pair (a, b) of a row at position p becomes
+ *   (a c - b s, a s + b c),  c = mscale cos(p f_i),  s = mscale sin(p f_i).
+ * The angle, its cosine and sine are computed in f64 (an f32 angle is off by
+ * 0.06 at position 10^6) and rounded once to f32; the products and the sum are
+ * f32, each rounded, and the result is rounded once to the rows' type.
+ * inverse != 0 rotates by -p: the gradient of x from the gradient of y.
+ *   x, y : rows [T][H][D], D % 4 == 0, 4 <= D <= 256.  y may be x itself (the
+ *          same pointer and strides); any other overlap is not allowed.
+ *   positions : int32 [T], device. */
+qmm_status qmm_rope(const qmm_rope_plan *plan, const void *x, void *y, int dtype, const int32_t *positions,
+                    int inverse, int64_t T, int64_t H, int64_t D, int64_t x_token_stride, int64_t x_head_stride,
+                    int64_t y_token_stride, int64_t y_head_stride, void *stream);
+
+/* The paged key-value cache of one layer: n_pages pages of `page` positions for
+ * all H key heads.  Slot s is position s % page of page s / page; which page
+ * holds which part of which sequence is the caller's page table.
+ *   Formats: q8_0 (d = amax/127 as f16, code = rne(x * 127/amax)) and q4_0
+ *   (qmm_quantize_q4_0's rule), a block per 32 values of a row, the codes and
+ *   scales of the weight formats of these names; and f16.
+ *   Bytes.  A page holds, for each head, the keys' side and then the values'
+ *   side; a side is page/16 groups of codes, then (quantized formats) the f16
+ *   scales [page][D/32].  A group is 16 positions, arranged so that one wave
+ *   loads it in whole lines and holds an operand of a matrix instruction: lane
+ *   (g, r), g < 4, r < 16, owns L = D/4 values,
+ *     keys:   of position r, value 32b + 8g + i  at (b, i)    b < D/32, i < 8
+ *     values: of position 4g + i, value 32b + 2r + e at (i, b, e)   i < 4, e < 2
+ *   in that order: one byte each, code + 128 (q8_0); two to a byte, the first
+ *   low, code + 8 (q4_0); or an f16.  A lane's bytes are cut into units of U
+ *   bytes, U = 16 or the largest power of two that divides them, and unit u of
+ *   lane (g, r) is at byte ((4u + g) * 16 + r) * U of the group.
+ * Limits: D is 64, 96, 128, 192 or 256; page a power of two, 16 <= page <= 4096;
+ * H <= 4096. */
+typedef struct {
+    void *data;      /* device, n_pages * qmm_kv_page_bytes_<format>(page, heads, dim) bytes, 16-byte aligned */
+    int64_t n_pages;
+    int64_t page;    /* positions in a page */
+    int64_t heads;   /* H, key heads */
+    int64_t dim;     /* D, values of a key and of a value */
+} qmm_kv_cache;
+
+/* Bytes of one page; 0 for sizes outside the limits. */
+int64_t qmm_kv_page_bytes_f16(int64_t page, int64_t heads, int64_t dim);
+int64_t qmm_kv_page_bytes_q8_0(int64_t page, int64_t heads, int64_t dim);
+int64_t qmm_kv_page_bytes_q4_0(int64_t page, int64_t heads, int64_t dim);
+
+/* Write T tokens' keys and values, rows [T][H][D], quantized, into the slots.
+ *   slots : int64 [T], device.  A slot outside [0, n_pages * page) is skipped
+ *           (padding tokens); two tokens must not have the same slot. */
+qmm_status qmm_kv_write_f16(const qmm_kv_cache *cache, const void *k, const void *v, int dtype, const int64_t *slots,
+                            int64_t T, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                            int64_t v_head_stride, void *stream);
+qmm_status qmm_kv_write_q8_0(const qmm_kv_cache *cache, const void *k, const void *v, int dtype,
+                             const int64_t *slots, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, void *stream);
+qmm_status qmm_kv_write_q4_0(const qmm_kv_cache *cache, const void *k, const void *v, int dtype,
+                             const int64_t *slots, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/* The same with the rotation, in one launch: keys are rotated as qmm_rope does
+ * and quantized from the f32 result (not rounded to the rows' type between),
+ * queries are rotated into q_out, values are written as they are.
+ *   q, q_out  : rows [T][Hq][D]; q_out may be q itself.
+ *   positions : int32 [T], device. */
+qmm_status qmm_rope_kv_write_f16(const qmm_rope_plan *plan, const qmm_kv_cache *cache, const void *q, void *q_out,
+                                 const void *k, const void *v, int dtype, const int32_t *positions,
+                                 const int64_t *slots, int64_t T, int64_t Hq, int64_t q_token_stride,
+                                 int64_t q_head_stride, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                 int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                 int64_t v_head_stride, void *stream);
+qmm_status qmm_rope_kv_write_q8_0(const qmm_rope_plan *plan, const qmm_kv_cache *cache, const void *q, void *q_out,
+                                  const void *k, const void *v, int dtype, const int32_t *positions,
+                                  const int64_t *slots, int64_t T, int64_t Hq, int64_t q_token_stride,
+                                  int64_t q_head_stride, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                  int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                  int64_t v_head_stride, void *stream);
+qmm_status qmm_rope_kv_write_q4_0(const qmm_rope_plan *plan, const qmm_kv_cache *cache, const void *q, void *q_out,
+                                  const void *k, const void *v, int dtype, const int32_t *positions,
+                                  const int64_t *slots, int64_t T, int64_t Hq, int64_t q_token_stride,
+                                  int64_t q_head_stride, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                  int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                  int64_t v_head_stride, void *stream);
+
+/* Read slots back as rows: code times scale, exact in f32, rounded once to the
+ * rows' type.  A slot outside [0, n_pages * page) gives rows of quiet NaNs.
+ *   k, v : rows [T][H][D], written; either may be NULL. */
+qmm_status qmm_kv_read_f16(const qmm_kv_cache *cache, const int64_t *slots, void *k, void *v, int dtype, int64_t T,
+                           int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                           int64_t v_head_stride, void *stream);
+qmm_status qmm_kv_read_q8_0(const qmm_kv_cache *cache, const int64_t *slots, void *k, void *v, int dtype, int64_t T,
+                            int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                            int64_t v_head_stride, void *stream);
+qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, void *k, void *v, int dtype, int64_t T,
+                            int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                            int64_t v_head_stride, void *stream);
+
+/* Attention of one new token of each of B sequences over its cache.  For query
+ * head h, which reads key head h / (Hq/H), and the positions t that are seen,
+ *   s_t = z + mask[b][t],   z = scale * q.k_t, or softcap * tanh(scale * q.k_t / softcap),
+ *   out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = ln sum_t exp(s_t).
+ * Position t is seen when t < lens[b], t >= lens[b] - window (window > 0) and
+ * mask[b][t] is not -inf; nothing that the cache holds elsewhere, NaN included,
+ * reaches a result.  With no position seen, out is 0 and lse is -inf.  A
+ * sequence whose length is outside [0, max_len], or with a page number outside
+ * [0, n_pages) under a position that lens and window leave, gives NaN (no read
+ * outside the cache).  Scores, weights and sums are f32; products run on f16
+ * matrix instructions with both factors exact or split into two f16 parts
+ * (22 bits).  Results do not depend on what runs beside the call: sums are
+ * joined in a fixed order.
+ *   q, out : rows [B][Hq][D], Hq a multiple of H.
+ *   pages  : int32 [B][pages_stride], device: page numbers of positions 0..page-1,
+ *            page.., as many as max_len needs; entries past a sequence are not read.
+ *   lens   : int32 [B], device.
+ *   max_len: 1 <= max_len <= pages_stride * page, a bound on lens known to the
+ *            host; the work is split by it.
+ *   softcap: 0 = none.   window: 0 = all positions.
+ *   mask   : f32 [B][mask_stride], mask_stride >= max_len, or NULL.
+ *   lse    : f32 [B][Hq], written, or NULL.
+ *   workspace : device, 16-byte aligned, at least qmm_attn_decode_workspace(...)
+ *            bytes for the same arguments (or larger B or max_len), filled with
+ *            zeros once before its first use; every call leaves it ready for the
+ *            next.  Calls that may run at the same time need one each.
+ * QMM_E_SHAPE also for a workspace that is too small. */
+int64_t qmm_attn_decode_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t max_len,
+                                  int64_t window);
+qmm_status qmm_attn_decode_f16(const qmm_kv_cache *cache, const void *q, void *out, int dtype, const int32_t *pages,
+                               int64_t pages_stride, const int32_t *lens, int64_t B, int64_t Hq, int64_t max_len,
+                               float scale, float softcap, int64_t window, const float *mask, int64_t mask_stride,
+                               float *lse, int64_t q_token_stride, int64_t q_head_stride, int64_t out_token_stride,
+                               int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
+qmm_status qmm_attn_decode_q8_0(const qmm_kv_cache *cache, const void *q, void *out, int dtype, const int32_t *pages,
+                                int64_t pages_stride, const int32_t *lens, int64_t B, int64_t Hq, int64_t max_len,
+                                float scale, float softcap, int64_t window, const float *mask, int64_t mask_stride,
+                                float *lse, int64_t q_token_stride, int64_t q_head_stride, int64_t out_token_stride,
+                                int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
+qmm_status qmm_attn_decode_q4_0(const qmm_kv_cache *cache, const void *q, void *out, int dtype, const int32_t *pages,
+                                int64_t pages_stride, const int32_t *lens, int64_t B, int64_t Hq, int64_t max_len,
+                                float scale, float softcap, int64_t window, const float *mask, int64_t mask_stride,
+                                float *lse, int64_t q_token_stride, int64_t q_head_stride, int64_t out_token_stride,
+                                int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,9 @@ supplies device memory and the current stream), every step of the
 computation runs in the library's HIP kernels.  There is no CPU fallback: if
 the library is missing or refuses a call, an exception is raised.
 
+The attention operators (rotary positions, paged key-value cache, decode
+attention) are in attention.py and reached from here.
+
 Byte layouts (see the header): Q8_0 34 B / 32 values, Q4_0 18 B / 32,
 Q2_K 84 B / 256, Q8_K 292 B / 256.
 """
@@ -15,6 +18,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+
+from . import attention as _attention
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmm.so")
@@ -72,6 +77,7 @@ def lib() -> ctypes.CDLL:
         for name in ["qmm_matmul_" + f for f in WEIGHT_FORMATS]:
             getattr(L, name).argtypes = [P, P, P, I64, I64, I64, P]
             getattr(L, name).restype = ctypes.c_int
+        _attention.declare(L)
         _lib = L
     return _lib
 
@@ -79,7 +85,7 @@ def lib() -> ctypes.CDLL:
 EXPORTS = tuple(["qmm_status_string", "qmm_abi_version", "qmm_quantize_q8_k"] +
                 ["qmm_quantize_matvec_" + f for f in FUSED_FORMATS] +
                 [p + f for p in ("qmm_quantize_", "qmm_matvec_", "qmm_matmul_", "qmm_get_rows_")
-                 for f in WEIGHT_FORMATS])
+                 for f in WEIGHT_FORMATS]) + _attention.EXPORTS
 
 
 def row_bytes(fmt: str, K: int) -> int:
@@ -275,3 +281,11 @@ QUANTIZE_MATVEC = {"q4_0": qmm_quantize_matvec_q4_0, "q8_0": qmm_quantize_matvec
                    "q2_k": qmm_quantize_matvec_q2_k, "q4_k": qmm_quantize_matvec_q4_k,
                    "q6_k": qmm_quantize_matvec_q6_k}
 GET_ROWS = {f: globals()["qmm_get_rows_" + f] for f in WEIGHT_FORMATS}
+
+# -- attention ------------------------------------------------------------------
+KV_FORMATS = _attention.KV_FORMATS
+RopePlan, KVCache = _attention.RopePlan, _attention.KVCache
+kv_page_bytes, attn_workspace = _attention.kv_page_bytes, _attention.attn_workspace
+KV_WRITE, ROPE_KV_WRITE, KV_READ = _attention.KV_WRITE, _attention.ROPE_KV_WRITE, _attention.KV_READ
+ATTN_DECODE = _attention.ATTN_DECODE
+globals().update({name: getattr(_attention, name) for name in _attention.EXPORTS})

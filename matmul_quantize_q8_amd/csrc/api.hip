@@ -1,10 +1,6 @@
 // C ABI of libqmm: argument checks, device check, launch.  Declarations and
 // the contract of every entry point are in include/qmm.h.
-#include <atomic>
-#include <cstring>
-
-#include "qmm.h"
-#include "qmm_device.h"
+#include "api_check.h"
 
 namespace qmm {
 hipError_t launch_quantize_q8_0(const float *x, void *out, int64_t nblocks, hipStream_t st);
@@ -51,26 +47,12 @@ int64_t matmul_k_max_blocks();
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxBytes = int64_t(1) << 40;
-constexpr int kMaxDevices = 64;
-
-std::atomic<int> g_device_state[kMaxDevices];   // 0 unknown, 1 gfx950, 2 other
-
-qmm_status check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return QMM_E_DEVICE;
-    int s = g_device_state[dev].load(std::memory_order_acquire);
-    if (s == 0) {
-        hipDeviceProp_t p;
-        if (hipGetDeviceProperties(&p, dev) != hipSuccess) return QMM_E_DEVICE;
-        s = (std::strncmp(p.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
-        g_device_state[dev].store(s, std::memory_order_release);
-    }
-    return s == 1 ? QMM_OK : QMM_E_DEVICE;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using qmm::aligned16;
+using qmm::check_device;
+using qmm::check_ptrs;
+using qmm::kMaxBytes;
+using qmm::kMaxDim;
+using qmm::launched;
 
 // rows x (K / blk) blocks of `bytes` each must stay below kMaxBytes.
 bool size_ok(int64_t rows, int64_t K, int64_t blk, int64_t bytes) {
@@ -87,16 +69,6 @@ qmm_status check_shape(int64_t M, int64_t N, int64_t K, int64_t blk) {
     if (K < blk || K > kMaxDim || K % blk != 0) return QMM_E_SHAPE;
     return QMM_OK;
 }
-
-qmm_status check_ptrs(std::initializer_list<const void *> ps) {
-    for (const void *p : ps)
-        if (p == nullptr) return QMM_E_NULL;
-    for (const void *p : ps)
-        if (!aligned16(p)) return QMM_E_ALIGN;
-    return QMM_OK;
-}
-
-qmm_status launched(hipError_t e) { return e == hipSuccess ? QMM_OK : QMM_E_LAUNCH; }
 
 typedef hipError_t (*quant_launch)(const float *, void *, int64_t, hipStream_t);
 

@@ -1,0 +1,282 @@
+// Rows in f32 / f16 / bf16, the rotation of a row's values, and the byte
+// layout of the paged key-value cache (include/qmm.h states the layout).
+#pragma once
+
+#include "qmm_device.h"
+
+namespace qmm {
+
+// Row types (qmm_dtype) and cache formats.
+enum RowType { R_F32 = 0, R_F16 = 1, R_BF16 = 2 };
+enum KvFmt { KV_F16 = 0, KV_Q8_0 = 1, KV_Q4_0 = 2 };
+
+constexpr int kMaxHeadDim = 256;
+
+constexpr int row_type_bytes(int rt) { return rt == R_F32 ? 4 : 2; }
+
+// One rounding, to nearest even; NaN stays a NaN.
+__device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
+    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+}
+
+template <int RT>
+__device__ __forceinline__ float load1(const void *base, int64_t i) {
+    if constexpr (RT == R_F32) return static_cast<const float *>(base)[i];
+    const uint32_t h = static_cast<const uint16_t *>(base)[i];
+    if constexpr (RT == R_F16) return f16_bits_to_f32(h);
+    return __builtin_bit_cast(float, h << 16);
+}
+
+// Four consecutive values; i is a multiple of four and the base is aligned to four elements.
+template <int RT>
+__device__ __forceinline__ float4 load4(const void *base, int64_t i) {
+    if constexpr (RT == R_F32) {
+        return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + i);
+        if constexpr (RT == R_F16)
+            return make_float4(f16_bits_to_f32(u.x), f16_bits_to_f32(u.x >> 16), f16_bits_to_f32(u.y),
+                               f16_bits_to_f32(u.y >> 16));
+        return make_float4(__builtin_bit_cast(float, u.x << 16), __builtin_bit_cast(float, u.x & 0xffff0000u),
+                           __builtin_bit_cast(float, u.y << 16), __builtin_bit_cast(float, u.y & 0xffff0000u));
+    }
+}
+
+template <int RT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (RT == R_F16) return f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16);
+    return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16);
+}
+
+template <int RT>
+__device__ __forceinline__ void store4(void *base, int64_t i, float4 v) {
+    if constexpr (RT == R_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + i) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) =
+            make_uint2(pack2<RT>(v.x, v.y), pack2<RT>(v.z, v.w));
+}
+
+template <int RT>
+__device__ __forceinline__ void store1(void *base, int64_t i, float v) {
+    if constexpr (RT == R_F32)
+        static_cast<float *>(base)[i] = v;
+    else
+        static_cast<uint16_t *>(base)[i] = (uint16_t)(RT == R_F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v));
+}
+
+// ---------------------------------------------------------------------------
+// Rotation
+// ---------------------------------------------------------------------------
+
+// Cosine and sine of an f64 angle, to about 1e-15: the angle less the nearest
+// multiple n of pi/2 (two-part constant, exact products through fma; |n| is
+// below 2^33 for any int32 position and frequency of at most pi), then the
+// Taylor polynomials on [-pi/4, pi/4], whose first dropped terms are
+// (pi/4)^17/17! = 5e-17 and (pi/4)^16/16! = 1e-15.
+__device__ __forceinline__ void cos_sin(double a, double &c, double &s) {
+    const double n = rint(a * 0.63661977236758134308);
+    double r = fma(-n, 1.57079632679489655800e+00, a);
+    r = fma(-n, 6.12323399573676603587e-17, r);
+    const double z = r * r;
+    double p = -1.0 / 1307674368000.0;
+    p = fma(p, z, 1.0 / 6227020800.0);
+    p = fma(p, z, -1.0 / 39916800.0);
+    p = fma(p, z, 1.0 / 362880.0);
+    p = fma(p, z, -1.0 / 5040.0);
+    p = fma(p, z, 1.0 / 120.0);
+    p = fma(p, z, -1.0 / 6.0);
+    const double sr = fma(p * z, r, r);
+    double q = -1.0 / 87178291200.0;
+    q = fma(q, z, 1.0 / 479001600.0);
+    q = fma(q, z, -1.0 / 3628800.0);
+    q = fma(q, z, 1.0 / 40320.0);
+    q = fma(q, z, -1.0 / 720.0);
+    q = fma(q, z, 1.0 / 24.0);
+    q = fma(q, z, -0.5);
+    const double cr = fma(q, z, 1.0);
+    const int k = (int)((long long)n & 3);
+    const double ss = (k & 1) ? cr : sr, cc = (k & 1) ? sr : cr;
+    s = (k & 2) ? -ss : ss;
+    c = (k == 1 || k == 2) ? -cc : cc;
+}
+
+struct Rope {
+    const double *freqs;
+    int rot, order, inverse;
+    float mscale;
+};
+
+// The token's cosines and sines into LDS, one pair a thread; the caller has a
+// barrier between this and rotate4.
+__device__ __forceinline__ void rope_table(const Rope &r, int32_t pos, float2 *cs, int tid, int threads) {
+    for (int i = tid; i < r.rot / 2; i += threads) {
+        double c, s;
+        cos_sin((double)pos * r.freqs[i], c, s);
+        cs[i] = make_float2((float)(c * (double)r.mscale), (float)(s * (double)r.mscale));
+        if (r.inverse) cs[i].y = -cs[i].y;
+    }
+}
+
+// Values n .. n+3 of the rotated row that starts at element `row` of `base`.
+// The pair's other value is read from memory again: the row is in the cache.
+template <int RT>
+__device__ __forceinline__ float4 rotate4(const void *base, int64_t row, int n, const Rope &r, const float2 *cs) {
+    const float4 x4 = load4<RT>(base, row + n);
+    if (n >= r.rot) return x4;
+    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+    float y[4];
+    if (r.order) {                                        // interleaved: both values of a pair are here
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            const bool in = n + k < r.rot;
+            const float2 t = cs[in ? (n + k) >> 1 : 0];
+            y[k] = in ? x[k] * t.x - x[k + 1] * t.y : x[k];
+            y[k + 1] = in ? x[k] * t.y + x[k + 1] * t.x : x[k + 1];
+        }
+    } else {
+        const int half = r.rot >> 1;
+        if ((half & 3) == 0) {                            // the four partners are aligned together
+            const bool first = n < half;
+            const int pair = first ? n : n - half;
+            const float4 p4 = load4<RT>(base, row + (first ? n + half : pair));
+            const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 t = cs[pair + k];
+                y[k] = first ? x[k] * t.x - p[k] * t.y : p[k] * t.y + x[k] * t.x;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = n + k;
+                y[k] = x[k];
+                if (i < r.rot) {
+                    const bool first = i < half;
+                    const int pair = first ? i : i - half;
+                    const float2 t = cs[pair];
+                    const float p = load1<RT>(base, row + (first ? i + half : pair));
+                    y[k] = first ? x[k] * t.x - p * t.y : p * t.y + x[k] * t.x;
+                }
+            }
+        }
+    }
+    return make_float4(y[0], y[1], y[2], y[3]);
+}
+
+// ---------------------------------------------------------------------------
+// The cache
+// ---------------------------------------------------------------------------
+constexpr int kGroup = 16;      // positions of a group of codes
+
+constexpr int kv_bits(int fmt) { return fmt == KV_F16 ? 16 : fmt == KV_Q8_0 ? 8 : 4; }
+
+// Sizes of a format at D = 32 * NB values a row.
+template <int F, int NB>
+struct Kv {
+    static constexpr int D = 32 * NB;
+    static constexpr bool kScaled = F != KV_F16;
+    static constexpr int L = NB * kv_bits(F);                       // bytes of a lane in a group (8 * NB values)
+    static constexpr int U = L % 16 == 0 ? 16 : L % 8 == 0 ? 8 : 4;  // bytes of a unit
+    static constexpr int NU = L / U;
+    static constexpr int kGroupBytes = 64 * L;
+    static constexpr int W = L / 4;                                 // bytes of one position in a value lane
+
+    __host__ __device__ static constexpr int64_t side_bytes(int64_t page) {
+        return page / kGroup * kGroupBytes + (kScaled ? page * NB * 2 : 0);
+    }
+    // Byte of a group that holds byte j of lane (g, r).
+    __host__ __device__ static constexpr int at(int g, int r, int j) {
+        return ((j / U * 4 + g) * 16 + r) * U + j % U;
+    }
+    // Byte of a lane that holds its value number v.
+    __host__ __device__ static constexpr int byte_of(int v) { return v * kv_bits(F) / 8; }
+
+    // Where quad `quad` (values 4 quad .. +3) of the row of position t lies in
+    // its group.  A key's four are consecutive; a value's are two lanes' two.
+    __host__ __device__ static constexpr int key_byte(int t, int quad) {
+        return at((quad & 7) >> 1, t & 15, byte_of((quad >> 3) * 8 + (quad & 1) * 4));
+    }
+    __host__ __device__ static constexpr int value_byte(int t, int quad, int second) {
+        return at((t & 15) >> 2, (quad & 7) * 2 + second, byte_of((t & 3) * 2 * NB + (quad >> 3) * 2));
+    }
+};
+
+constexpr int64_t kv_page_bytes(int fmt, int64_t page, int64_t heads, int64_t dim) {
+    return heads * 2 * (page * dim * kv_bits(fmt) / 8 + (fmt == KV_F16 ? 0 : page * dim / 32 * 2));
+}
+
+struct KvCache {
+    uint8_t *data;
+    int64_t n_pages;
+    int page_shift;             // log2 of the positions in a page
+    int heads;
+
+    __host__ __device__ bool has_page(int64_t p) const { return p >= 0 && p < n_pages; }
+    // The sides of head h of a page it has: keys at 2h * side, values at (2h + 1) * side.
+    __host__ __device__ uint8_t *page_at(int64_t p, int64_t side) const { return data + p * heads * 2 * side; }
+};
+
+// Strides of rows, in elements.
+struct Strides {
+    int64_t token, head;
+};
+
+struct WriteArgs {
+    Rope r;                     // rot = 0: nothing is rotated
+    KvCache c;
+    const void *q, *k, *v;
+    void *qo;
+    const int32_t *positions;
+    const int64_t *slots;
+    int Hq;                     // 0: no queries
+    Strides qs, qos, ks, vs;
+};
+
+struct ReadArgs {
+    KvCache c;
+    const int64_t *slots;
+    void *k, *v;                // NULL: not wanted
+    Strides ks, vs;
+};
+
+struct AttnArgs {
+    KvCache c;
+    const void *q;
+    void *out;
+    const int32_t *pages, *lens;
+    int64_t pages_stride;
+    const float *mask;          // NULL: none
+    int64_t mask_stride;
+    float *lse;                 // NULL: not wanted
+    float *part;                // [B * Hq][splits][D] partial sums
+    float2 *part_ml;            // [B * Hq][splits] their maximum and sum of weights
+    int Hq, max_len, window, splits, chunk;
+    float scale, softcap;
+    Strides qs, os;
+};
+
+// Calls fn<format, D / 32>(arguments) for a checked format and D.
+#define QMM_KV_DISPATCH(fn, ...)                                     \
+    switch (fmt * 16 + nb) {                                         \
+        case KV_F16 * 16 + 2: return fn<KV_F16, 2>(__VA_ARGS__);     \
+        case KV_F16 * 16 + 3: return fn<KV_F16, 3>(__VA_ARGS__);     \
+        case KV_F16 * 16 + 4: return fn<KV_F16, 4>(__VA_ARGS__);     \
+        case KV_F16 * 16 + 6: return fn<KV_F16, 6>(__VA_ARGS__);     \
+        case KV_F16 * 16 + 8: return fn<KV_F16, 8>(__VA_ARGS__);     \
+        case KV_Q8_0 * 16 + 2: return fn<KV_Q8_0, 2>(__VA_ARGS__);   \
+        case KV_Q8_0 * 16 + 3: return fn<KV_Q8_0, 3>(__VA_ARGS__);   \
+        case KV_Q8_0 * 16 + 4: return fn<KV_Q8_0, 4>(__VA_ARGS__);   \
+        case KV_Q8_0 * 16 + 6: return fn<KV_Q8_0, 6>(__VA_ARGS__);   \
+        case KV_Q8_0 * 16 + 8: return fn<KV_Q8_0, 8>(__VA_ARGS__);   \
+        case KV_Q4_0 * 16 + 2: return fn<KV_Q4_0, 2>(__VA_ARGS__);   \
+        case KV_Q4_0 * 16 + 3: return fn<KV_Q4_0, 3>(__VA_ARGS__);   \
+        case KV_Q4_0 * 16 + 4: return fn<KV_Q4_0, 4>(__VA_ARGS__);   \
+        case KV_Q4_0 * 16 + 6: return fn<KV_Q4_0, 6>(__VA_ARGS__);   \
+        case KV_Q4_0 * 16 + 8: return fn<KV_Q4_0, 8>(__VA_ARGS__);   \
+    }                                                                \
+    return hipErrorInvalidValue
+
+}  // namespace qmm
