@@ -11,7 +11,7 @@ hipError_t launch_rope(int rt, Rope r, const void *x, void *y, const int32_t *po
 hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, int64_t T, hipStream_t st);
 hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, int64_t T, hipStream_t st);
 hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, hipStream_t st);
-int64_t attn_workspace(int64_t B, int64_t Hq, int64_t D, int64_t max_len, int64_t window);
+int64_t attn_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_len, int64_t window);
 }  // namespace qmm
 
 namespace {
@@ -131,8 +131,8 @@ qmm_status kv_read(int fmt, const qmm_kv_cache *cache, const int64_t *slots, voi
 // Bytes of the workspace; 0 for sizes outside the limits.
 int64_t workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t max_len, int64_t window) {
     if (B < 1 || B > 65535 || Hq < 1 || Hq > kMaxHeads || heads < 1 || heads > Hq || Hq % heads != 0) return 0;
-    if (!head_dim_ok(dim) || max_len < 1 || max_len > kMaxDim - 4096 || window < 0 || window > kMaxDim) return 0;
-    return attn_workspace(B, Hq, dim, max_len, window);
+    if (!head_dim_ok(dim) || max_len < 1 || max_len > kMaxDim - 8192 || window < 0 || window > kMaxDim) return 0;
+    return attn_workspace(B, Hq, heads, dim, max_len, window);
 }
 
 qmm_status attn_decode(int fmt, const qmm_kv_cache *cache, const void *q, void *out, int dtype, const int32_t *pages,
