@@ -23,6 +23,8 @@
 // The partial results of several chunks are joined by a second launch:
 //   M = max m,  l = sum l_i exp(m_i - M),  out = sum o_i exp(m_i - M) / l.
 #include "kv_layout.h"
+#include <cfloat>
+#include <type_traits>
 
 namespace qmm {
 
@@ -40,17 +42,17 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// Two f32 as two f16, to nearest even.
-__device__ __forceinline__ v2h to_halves(float a, float b) {
-    const v2f f = {a, b};
-    return __builtin_convertvector(f, v2h);
-}
-
-// a and b as hi + lo of two f16 each.
-__device__ __forceinline__ void split_halves(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const v2h h = to_halves(a, b);
+// a * x and b * y as hi + lo of two f16 each, x and y f16: hi is the product
+// rounded to nearest even, lo what is left of it (one fused operation each, whose
+// f16 factors and f16 result need no conversions of their own).
+__device__ __forceinline__ void split_products(float a, _Float16 x, float b, _Float16 y, uint32_t &hi, uint32_t &lo) {
+    const v2h h = {(_Float16)fmaf((float)x, a, 0.0f), (_Float16)fmaf((float)y, b, 0.0f)};
+    const v2h l = {(_Float16)fmaf((float)x, a, -(float)h.x), (_Float16)fmaf((float)y, b, -(float)h.y)};
     hi = __builtin_bit_cast(uint32_t, h);
-    lo = __builtin_bit_cast(uint32_t, to_halves(a - (float)h.x, b - (float)h.y));
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+__device__ __forceinline__ void split_halves(float a, float b, uint32_t &hi, uint32_t &lo) {
+    split_products(a, (_Float16)1.0f, b, (_Float16)1.0f, hi, lo);
 }
 
 // Maximum / sum over the four lanes n, n + 16, n + 32, n + 48, in all of them.
@@ -82,6 +84,15 @@ __device__ __forceinline__ float sum_rows(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// tanh to about 2^-22: Lambert's continued fraction, five levels deep, up to 0.6
+// (its first dropped part is below 1e-9 there), beyond that (e^2x - 1) / (e^2x + 1).
+__device__ __forceinline__ float tanh_f32(float x) {
+    const float y = fminf(fabsf(x), 20.0f), z = y * y, e = exp2_fast(2.0f * kLog2e * y);
+    const float num = y < 0.6f ? y * fmaf(z, fmaf(z, 21.0f, 1260.0f), 10395.0f) : e - 1.0f;
+    const float den = y < 0.6f ? fmaf(z, fmaf(z, z + 210.0f, 4725.0f), 10395.0f) : e + 1.0f;
+    return x != x ? x : copysignf(num / den, x);
+}
+
 // ---------------------------------------------------------------------------
 // A lane's bytes of a group, and its scales
 // ---------------------------------------------------------------------------
@@ -102,13 +113,15 @@ __device__ __forceinline__ void load_codes(const uint8_t *codes, int lane, uint3
     }
 }
 
-// The f16 scales of positions 4g .. 4g+3 of a group: [4][NB], two to a word.
+// A wave's scales of one side of a tile, [32][NB] halves in LDS: those of
+// positions 16 j + 4 g .. + 3, two to a word.
 template <int NB>
-__device__ __forceinline__ void load_scales(const uint8_t *scales, int g, uint32_t (&x)[2 * NB]) {
+__device__ __forceinline__ void read_scales(const uint32_t *sc, int j, int g, uint32_t (&x)[2 * NB]) {
     constexpr int B = NB % 2 ? 8 : 16;
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(sc + j * 8 * NB + g * 2 * NB);
 #pragma unroll
     for (int u = 0; u < 8 * NB / B; ++u) {
-        const Unit<B> v = *reinterpret_cast<const Unit<B> *>(scales + g * 8 * NB + u * B);
+        const Unit<B> v = *reinterpret_cast<const Unit<B> *>(p + u * B);
 #pragma unroll
         for (int i = 0; i < B / 4; ++i) x[u * (B / 4) + i] = v.w[i];
     }
@@ -116,20 +129,30 @@ __device__ __forceinline__ void load_scales(const uint8_t *scales, int g, uint32
 
 // Scale of position i, block b of such words.
 template <int NB>
-__device__ __forceinline__ float scale_of(const uint32_t (&x)[2 * NB], int i, int b) {
+__device__ __forceinline__ _Float16 scale_of(const uint32_t (&x)[2 * NB], int i, int b) {
     const int k = i * NB + b;
     const v2h h = __builtin_bit_cast(v2h, x[k >> 1]);
-    return (float)((k & 1) ? h.y : h.x);
+    return (k & 1) ? h.y : h.x;
 }
 
 // ---------------------------------------------------------------------------
 // Codes as operands
 // ---------------------------------------------------------------------------
-// Integers u < 256 in the low bytes of two halves are, as f16, u * 2^-24.  The
-// key product takes them so (its accumulator starts at the offset's share, and
-// its result is scaled by 2^24); the value product takes (u - offset) * 2^-9,
-// one packed multiply-add away.
-constexpr float kKeyUnit = 0x1p-24f, kValueUnit = 0x1p-9f;
+// Codes u as halves without an integer conversion: u in the low bits of a half
+// is, as f16, u * 2^-24, and one packed multiply-add makes it (u - offset) * 2^-9,
+// exactly.  (The product could take u * 2^-24 and have its accumulator start at
+// the offset's share.  That was tried, and cost accuracy: a matrix instruction
+// aligns its products by their exponent fields, so a subnormal's leading zeros
+// push out low bits.  Score errors were ten times as large with 4-bit codes.)
+template <int F> constexpr float kCodeUnit = F == KV_F16 ? 1.0f : 0x1p-9f;
+
+// Words of two codes each, at bit 0 (SHIFT = 0) or 4 of their halves.
+template <int F, int SHIFT>
+__device__ __forceinline__ uint32_t code_halves(uint32_t u) {
+    constexpr float unit = SHIFT == 4 ? 0x1p11f : 0x1p15f, offset = -(F == KV_Q8_0 ? 128.0f : 8.0f) * 0x1p-9f;
+    const v2h m = {(_Float16)unit, (_Float16)unit}, c = {(_Float16)offset, (_Float16)offset};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(v2h, u), m, c));
+}
 
 template <int F, int NB>
 __device__ __forceinline__ v4u key_operand(const uint32_t (&x)[Kv<F, NB>::L / 4], int b) {
@@ -140,12 +163,16 @@ __device__ __forceinline__ v4u key_operand(const uint32_t (&x)[Kv<F, NB>::L / 4]
     } else if constexpr (F == KV_Q8_0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            a[2 * j] = __builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c010c00u);
-            a[2 * j + 1] = __builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c030c02u);
+            a[2 * j] = code_halves<F, 0>(__builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c010c00u));
+            a[2 * j + 1] = code_halves<F, 0>(__builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c030c02u));
         }
     } else {                                    // pairs (j, j + 4): the queries are in that order too
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = (x[b] >> (4 * j)) & 0x000f000fu;
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t y = x[b] >> (8 * j);
+            a[2 * j] = code_halves<F, 0>(y & 0x000f000fu);
+            a[2 * j + 1] = code_halves<F, 4>(y & 0x00f000f0u);
+        }
     }
     return a;
 }
@@ -154,11 +181,6 @@ __device__ __forceinline__ v4u key_operand(const uint32_t (&x)[Kv<F, NB>::L / 4]
 template <int F>
 __device__ __forceinline__ constexpr int query_slot(int s) {
     return F == KV_Q4_0 ? (s >> 1) + 4 * (s & 1) : s;
-}
-
-__device__ __forceinline__ uint32_t offset_codes(uint32_t u, float unit, float offset) {
-    const v2h m = {(_Float16)unit, (_Float16)unit}, c = {(_Float16)offset, (_Float16)offset};
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(v2h, u), m, c));
 }
 
 // Values 32b + 2r + e of the lane's four positions of a group, as two words of
@@ -180,11 +202,11 @@ __device__ __forceinline__ void value_words(const uint32_t (&x)[Kv<F, NB>::L / 4
             const uint32_t u = __builtin_amdgcn_perm(q, p, sel);
             if constexpr (F == KV_Q8_0) {
                 const uint32_t v = __builtin_amdgcn_perm(q, p, sel + 0x00010001u);
-                lo[j] = offset_codes(u, 0x1p15f, -128.0f * kValueUnit);
-                hi[j] = offset_codes(v, 0x1p15f, -128.0f * kValueUnit);
+                lo[j] = code_halves<F, 0>(u);
+                hi[j] = code_halves<F, 0>(v);
             } else {
-                lo[j] = offset_codes(u & 0x000f000fu, 0x1p15f, -8.0f * kValueUnit);
-                hi[j] = offset_codes(u & 0x00f000f0u, 0x1p11f, -8.0f * kValueUnit);
+                lo[j] = code_halves<F, 0>(u & 0x000f000fu);
+                hi[j] = code_halves<F, 4>(u & 0x00f000f0u);
             }
         }
     }
@@ -193,20 +215,23 @@ __device__ __forceinline__ void value_words(const uint32_t (&x)[Kv<F, NB>::L / 4
 // ---------------------------------------------------------------------------
 // One chunk
 // ---------------------------------------------------------------------------
-// Weights of up to e^4 are let stand before the maximum is moved (moving it
-// multiplies every accumulator); they, the scales and the weights' factor stay
-// inside f16: e^4 * 2 * 2^8 = 27 955.  A value scale of 2 and more (values
-// beyond 254) drops the factor and the slack for the rest of the wave's tiles.
-constexpr float kMaxSlack = 4.0f, kWeightScale = 256.0f;
+// Scores are kept in log2 units.  A wave's weights are 2^(s - r) for a reference
+// r that lies kWeightBits under the largest score it was set by.  The reference is moved (which
+// multiplies every accumulator) only when a score passes that one by kSlackBits:
+// weights, times value scales below 2, stay inside f16 (2^(8 + 6 + 1) = 32 768),
+// and small ones keep their low parts out of its subnormals.  Tiles with a value
+// scale of 2 and more (values beyond 254) make the wave keep r at the maximum.
+constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f;
 
-template <int F, int NB, bool MASKED>
-__global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(AttnArgs a, int rt) {
+template <int F, int NB, int RT>
+__global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : NB == 6 ? 2 : 3) void k_attn_chunk(AttnArgs a) {
     using K = Kv<F, NB>;
     constexpr int D = 32 * NB, LW = K::L / 4;
     constexpr bool kScaled = K::kScaled;
-    // scores are kept in log2 units, or with a mask in natural ones (the lowest f32 has to stay finite)
-    constexpr float kUnit = MASKED ? 1.0f : kLog2e;
+    constexpr int SW = 16 * NB, SR = (SW + 63) / 64;      // words of a side's scales of a tile, and of a lane
     __shared__ float join[2 * (8 * NB + 2) * 64];
+    __shared__ v4u queries[2][NB][64];
+    __shared__ __attribute__((aligned(16))) uint32_t scales[kScaled ? kAttnWaves : 1][kScaled ? SW : 4];
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -216,6 +241,11 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
     const bool live = h0 + n < group;
     const int hq = kv * group + h0 + (live ? n : 0);
 
+    float4 qx[NB][2];
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k)
+        qx[k >> 1][k & 1] = load4<RT>(a.q, b * a.qs.token + hq * a.qs.head + (k >> 1) * 32 + g * 8 + (k & 1) * 4);
+
     const int len = a.lens[b], shift = a.c.page_shift, page = 1 << shift;
     const bool bad_len = len < 0 || len > a.max_len;
     const int lo = a.window && !bad_len ? max(0, len - a.window) : 0;
@@ -223,135 +253,183 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
     const int to = bad_len ? from : from + min(len - from, a.chunk);
     const int64_t side = K::side_bytes(page);
 
-    // The queries: scaled by a power of two to below 2^8, split in two f16.
-    v4u qh[NB], ql[NB];
-    float qoff[NB], unit;
-    {
-        float x[NB][8], top = 0.0f;
-        const int64_t row = b * a.qs.token + hq * a.qs.head;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-            for (int s = 0; s < 8; s += 4) {
-                const int64_t at = row + blk * 32 + g * 8 + s;
-                float4 v = rt == R_F32 ? load4<R_F32>(a.q, at)
-                                       : rt == R_F16 ? load4<R_F16>(a.q, at) : load4<R_BF16>(a.q, at);
-                if (!live) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                x[blk][s] = v.x;
-                x[blk][s + 1] = v.y;
-                x[blk][s + 2] = v.z;
-                x[blk][s + 3] = v.w;
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-            }
-        top = max_rows(top);
-        const int e = top > 0.0f && top < INFINITY ? min(max(7 - ilogbf(top), -120), 120) : 0;
-        const float up = ldexpf(1.0f, e);
-        unit = ldexpf(a.scale, -e) * (kScaled ? 0x1p24f : 1.0f);
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u = x[blk][query_slot<F>(2 * j)] * up, v = x[blk][query_slot<F>(2 * j + 1)] * up;
-                uint32_t hi, lw;
-                split_halves(u, v, hi, lw);
-                qh[blk][j] = hi;
-                ql[blk][j] = lw;
-                sum += u + v;
-            }
-            qoff[blk] = kScaled ? -(F == KV_Q8_0 ? 128.0f : 8.0f) * kKeyUnit * sum_rows(sum) : 0.0f;
-        }
-    }
-
-    v4f o[NB][2];
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) o[blk][0] = o[blk][1] = v4f{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.0f, factor = kWeightScale, slack = kMaxSlack * kUnit;
-
-    int pages = 0;                              // lane i: the page of the i-th group of this wave's next 32 tiles
+    // Tiles wave, wave + 4, ... of the chunk.  A tile's keys are loaded as soon as
+    // the last tile's are used up, and its values likewise, into the same
+    // registers: the loads have the other half of a tile's work to arrive in.
     const int ntiles = (to - from + kTile - 1) / kTile;
-    int count = 0;
-    for (int tile = wave; tile < ntiles; tile += kAttnWaves, ++count) {
-        if ((count & 31) == 0) {
-            const int t = from + (tile + (lane >> 1) * kAttnWaves) * kTile + (lane & 1) * kGroup;
-            pages = t < to ? a.pages[b * a.pages_stride + (t >> shift)] : 0;
+    int pages = 0;                              // lane i: the page of the i-th group of this wave's next 32 tiles
+    const uint8_t *kside[2];                    // the tile's groups: keys' side of the page and place in it
+    int place[2];
+    bool bad = false;
+    uint32_t kx[2][LW], vx[2][LW], ks[SR], vs[SR];
+    const auto look_up = [&](int tile) {
+        const int t = from + (tile + (lane >> 1) * kAttnWaves) * kTile + (lane & 1) * kGroup;
+        pages = t < to ? a.pages[b * a.pages_stride + (t >> shift)] : 0;
+    };
+    const auto locate = [&](int tile, int count) {
+        if (count > 0 && (count & 31) == 0) {
+            look_up(tile);
+            asm volatile("" : "+v"(pages));     // waited for here, not at every tile's readlane
         }
-        const int t0 = from + tile * kTile;
-        uint32_t kx[2][LW], vx[2][LW], ks[2][2 * NB], vs[2][2 * NB];
-        bool bad = false;
+        bad = false;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             // a second group past the end is not looked up: the first is read again and not used
-            const int t = t0 + j * kGroup < to ? t0 + j * kGroup : t0;
+            const int t0 = from + tile * kTile, t = t0 + j * kGroup < to ? t0 + j * kGroup : t0;
             int p = __builtin_amdgcn_readlane(pages, 2 * (count & 31) + (t != t0));
             if (!a.c.has_page(p)) {
                 bad = true;
                 p = 0;
             }
-            const uint8_t *kside = a.c.page_at(p, side) + 2 * kv * side, *vside = kside + side;
-            const int at = t & (page - 1);
-            load_codes<F, NB>(kside + (at >> 4) * K::kGroupBytes, lane, kx[j]);
-            if constexpr (kScaled) load_scales<NB>(kside + (page >> 4) * K::kGroupBytes + at * NB * 2, g, ks[j]);
-            load_codes<F, NB>(vside + (at >> 4) * K::kGroupBytes, lane, vx[j]);
-            if constexpr (kScaled) load_scales<NB>(vside + (page >> 4) * K::kGroupBytes + at * NB * 2, g, vs[j]);
+            kside[j] = a.c.page_at(p, side) + 2 * kv * side;
+            place[j] = t & (page - 1);
         }
+    };
+    const auto load = [&](bool values, uint32_t(&x)[2][LW], uint32_t(&sc)[SR]) {
+        const int64_t off = values ? side : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            load_codes<F, NB>(kside[j] + off + (place[j] >> 4) * K::kGroupBytes, lane, x[j]);
+        if constexpr (kScaled) {
+            const uint8_t *s0 = kside[0] + off + (page >> 4) * K::kGroupBytes + place[0] * NB * 2;
+            const uint8_t *s1 = kside[1] + off + (page >> 4) * K::kGroupBytes + place[1] * NB * 2;
+#pragma unroll
+            for (int k = 0; k < SR; ++k) {
+                const int i = lane + 64 * k;
+                if (SW % 64 == 0 || i < SW)
+                    sc[k] = *reinterpret_cast<const uint32_t *>(i < 8 * NB ? s0 + 4 * i : s1 + 4 * (i - 8 * NB));
+            }
+        }
+    };
+    uint32_t *const sc = scales[kScaled ? wave : 0];
+    const auto stage = [&](const uint32_t(&x)[SR]) {
+#pragma unroll
+        for (int k = 0; k < SR; ++k)
+            if (SW % 64 == 0 || lane + 64 * k < SW) sc[lane + 64 * k] = x[k];
+        __builtin_amdgcn_wave_barrier();
+    };
+    look_up(wave);
+    asm volatile("" : "+v"(pages));             // and the queries with them: no wait for them reaches past the tile's loads
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) asm volatile("" : "+v"(qx[k >> 1][k & 1].x));
+    if (wave < ntiles) {
+        locate(wave, 0);
+        load(false, kx, ks);
+        load(true, vx, vs);
+    }
+
+    // The queries: scaled by a power of two to below 2^8, split in two f16, in LDS.
+    float unit;
+    {
+        float x[NB][8], top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k) {
+            const float4 v = qx[k >> 1][k & 1];
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[k >> 1][(k & 1) * 4 + i] = live ? f[i] : 0.0f;
+                top = fmaxf(top, live ? fabsf(f[i]) : 0.0f);
+            }
+        }
+        top = max_rows(top);
+        const int e = top > 0.0f && top < INFINITY ? min(max(7 - ilogbf(top), -120), 120) : 0;
+        const float up = ldexpf(1.0f, e);
+        unit = ldexpf(a.scale, -e) / kCodeUnit<F>;    // of the products: the score's natural units
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            if ((blk & (kAttnWaves - 1)) != wave) continue;   // every wave has them all and writes its share
+            v4u hi, lw;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t h, w;
+                split_halves(x[blk][query_slot<F>(2 * j)] * up, x[blk][query_slot<F>(2 * j + 1)] * up, h, w);
+                hi[j] = h;
+                lw[j] = w;
+            }
+            queries[0][blk][lane] = hi;
+            queries[1][blk][lane] = lw;
+        }
+    }
+    __syncthreads();
+
+    v4f o[NB][2];
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) o[blk][0] = o[blk][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    float r = -INFINITY, l = 0.0f, under = kWeightBits, most = kWeightBits + kSlackBits;
+
+    const float capped = a.softcap > 0.0f ? unit / a.softcap : 0.0f;
+    int count = 0;
+    const auto step = [&](int tile, auto last) {
+        constexpr bool more = !decltype(last)::value;
+        const int t0 = from + tile * kTile;
+        const bool was_bad = bad;
+        ++count;
 
         // scores of positions t0 + 16 j + 4 g + i
         float s[2][4];
+        if constexpr (kScaled) stage(ks);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+            uint32_t kd[2 * NB];
+            if constexpr (kScaled) read_scales<NB>(sc, j, g, kd);
             v4f z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
                 const v4u key = key_operand<F, NB>(kx[j], blk);
                 if constexpr (kScaled) {
-                    v4f acc = {qoff[blk], qoff[blk], qoff[blk], qoff[blk]};
-                    acc = mfma(key, qh[blk], acc);
-                    acc = mfma(key, ql[blk], acc);
+                    v4f acc = mfma(key, queries[0][blk][lane], v4f{0.f, 0.f, 0.f, 0.f});
+                    acc = mfma(key, queries[1][blk][lane], acc);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = fmaf(scale_of<NB>(ks[j], i, blk), acc[i], z[i]);
+                    for (int i = 0; i < 4; ++i) z[i] = fmaf((float)scale_of<NB>(kd, i, blk), acc[i], z[i]);
                 } else {
-                    z = mfma(key, qh[blk], z);
-                    z = mfma(key, ql[blk], z);
+                    z = mfma(key, queries[0][blk][lane], z);
+                    z = mfma(key, queries[1][blk][lane], z);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = z[i] * unit;
+            for (int i = 0; i < 4; ++i) s[j][i] = z[i];
+        }
+        if constexpr (more) {
+            locate(tile + kAttnWaves, count);
+            load(false, kx, ks);
         }
         if (a.softcap > 0.0f) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k >> 2][k & 3] = a.softcap * tanhf(s[k >> 2][k & 3] / a.softcap);
-        }
-        if constexpr (!MASKED) {
+            for (int k = 0; k < 8; ++k)
+                s[k >> 2][k & 3] = a.softcap * kLog2e * tanh_f32(s[k >> 2][k & 3] * capped);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k >> 2][k & 3] *= kLog2e;
+            for (int k = 0; k < 8; ++k) s[k >> 2][k & 3] *= unit * kLog2e;
         }
-        if (bad) {
+        if (was_bad) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[k >> 2][k & 3] = NAN;
         }
-        if (MASKED || t0 < lo || t0 + kTile > to) {   // some positions may not be seen: whatever they hold is dropped
+        if (a.mask || t0 < lo || t0 + kTile > to) {   // some positions may not be seen: whatever they hold is dropped
+            const auto extra = [&](int t) {           // what the mask adds; -inf: not seen
+                if (t < lo || t >= to) return -INFINITY;
+                if (!a.mask) return 0.0f;
+                const float x = a.mask[b * a.mask_stride + t];
+                return x == -INFINITY ? x : fmaxf(x * kLog2e, -FLT_MAX);
+            };
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const int j = k >> 2, i = k & 3, t = t0 + j * kGroup + 4 * g + i;
-                bool seen = t >= lo && t < to;
-                if constexpr (MASKED) {
-                    const float x = seen ? a.mask[b * a.mask_stride + t] : -INFINITY;
-                    seen = x != -INFINITY;
-                    s[j][i] += x;
+                const int j = k >> 2, i = k & 3;
+                const float x = extra(t0 + j * kGroup + 4 * g + i);
+                s[j][i] = x == -INFINITY ? -INFINITY : s[j][i] + x;
+                if constexpr (!kScaled) {
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk)
+                        if (x == -INFINITY) vx[j][i * NB + blk] = 0u;
                 }
-                if (!seen) {
-                    s[j][i] = -INFINITY;
-                    if constexpr (kScaled) {
+            }
+            if constexpr (kScaled) {                  // codes are finite, scales need not be
 #pragma unroll
-                        for (int blk = 0; blk < NB; ++blk) {
-                            const int w = i * NB + blk;
-                            vs[j][w >> 1] &= (w & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    } else {
-#pragma unroll
-                        for (int blk = 0; blk < NB; ++blk) vx[j][i * NB + blk] = 0u;
-                    }
+                for (int k = 0; k < SR; ++k) {
+                    const int h = 2 * (lane + 64 * k);
+                    if (extra(t0 + h / NB) == -INFINITY) vs[k] &= 0xffff0000u;
+                    if (extra(t0 + (h + 1) / NB) == -INFINITY) vs[k] &= 0x0000ffffu;
                 }
             }
         }
@@ -359,26 +437,18 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
         if constexpr (kScaled) {
             uint32_t any = 0;
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) any |= vs[0][i] | vs[1][i];
-            if (factor != 1.0f && __any((any & 0x40004000u) != 0)) {
-                factor = 1.0f;
-                slack = 0.0f;
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        o[blk][0][i] *= 1.0f / kWeightScale;
-                        o[blk][1][i] *= 1.0f / kWeightScale;
-                    }
-            }
+            for (int k = 0; k < SR; ++k)
+                if (SW % 64 == 0 || lane + 64 * k < SW) any |= vs[k];
+            if (__any((any & 0x40004000u) != 0)) under = most = 0.0f;
+            stage(vs);
         }
         float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                           fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
         top = max_rows(top);
-        if (__any(top > m + slack)) {
-            const float next = fmaxf(m, top);
-            const float alpha = m == next ? 1.0f : exp2_fast((m - next) * (kLog2e / kUnit));
-            m = next;
+        if (__any(top > r + most)) {
+            const float next = fmaxf(r, top - under);
+            const float alpha = r == next ? 1.0f : exp2_fast(r - next);
+            r = next;
             l *= alpha;
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk)
@@ -388,29 +458,30 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
                     o[blk][1][i] *= alpha;
                 }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = r == -INFINITY ? 0.0f : r;
         float p[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float d = s[k >> 2][k & 3] - base;
-            p[k] = exp2_fast(MASKED ? d * kLog2e : d);
+            p[k] = exp2_fast(s[k >> 2][k & 3] - base);
             l += p[k];
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] *= factor;
+        uint32_t vd[2][2 * NB];
+        if constexpr (kScaled) {
+            read_scales<NB>(sc, 0, g, vd[0]);
+            read_scales<NB>(sc, 1, g, vd[1]);
+        }
         v4u wh, wl;
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
             if (kScaled || blk == 0) {
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
-                    float u = p[k], v = p[k + 1];
-                    if constexpr (kScaled) {
-                        u *= scale_of<NB>(vs[k >> 2], k & 3, blk);
-                        v *= scale_of<NB>(vs[k >> 2], (k & 3) + 1, blk);
-                    }
                     uint32_t hi, lw;
-                    split_halves(u, v, hi, lw);
+                    if constexpr (kScaled)
+                        split_products(p[k], scale_of<NB>(vd[k >> 2], k & 3, blk), p[k + 1],
+                                       scale_of<NB>(vd[k >> 2], (k & 3) + 1, blk), hi, lw);
+                    else
+                        split_halves(p[k], p[k + 1], hi, lw);
                     wh[k >> 1] = hi;
                     wl[k >> 1] = lw;
                 }
@@ -424,34 +495,41 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
             o[blk][0] = mfma(va, wl, o[blk][0]);
             o[blk][1] = mfma(vb, wl, o[blk][1]);
         }
-    }
+        if constexpr (more) load(true, vx, vs);
+    };
+    // The last tile is a call of its own: with one loop and a condition on the
+    // loads, every tile waits for all of them.
+    int tile = wave;
+    for (; tile + kAttnWaves < ntiles; tile += kAttnWaves) step(tile, std::false_type{});
+    if (tile < ntiles) step(tile, std::true_type{});
 
     // The wave's result, then the four waves' in a fixed order: 0 + 2, 1 + 3, both.
     l = sum_rows(l);
-    const float back = (kScaled ? 1.0f / kValueUnit : 1.0f) / factor;
+    if constexpr (kScaled) {
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
+        for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[blk][0][i] *= back;
-            o[blk][1][i] *= back;
-        }
+            for (int i = 0; i < 4; ++i) {
+                o[blk][0][i] *= 1.0f / kCodeUnit<F>;
+                o[blk][1][i] *= 1.0f / kCodeUnit<F>;
+            }
+    }
 #pragma unroll
     for (int step = 2; step > 0; step >>= 1) {
         float *slot = join + (wave & (step - 1)) * (8 * NB + 2) * 64 + lane;
         if (step == 1) __syncthreads();
         if (wave >= step && wave < 2 * step) {
-            slot[0] = m;
+            slot[0] = r;
             slot[64] = l;
 #pragma unroll
             for (int k = 0; k < 8 * NB; ++k) slot[(2 + k) * 64] = o[k >> 3][(k >> 2) & 1][k & 3];
         }
         __syncthreads();
         if (wave < step) {
-            const float m2 = slot[0], l2 = slot[64], top = fmaxf(m, m2);
+            const float r2 = slot[0], l2 = slot[64], top = fmaxf(r, r2);
             const float base = top == -INFINITY ? 0.0f : top;
-            const float w1 = exp2_fast((m - base) * (kLog2e / kUnit)), w2 = exp2_fast((m2 - base) * (kLog2e / kUnit));
-            m = top;
+            const float w1 = exp2_fast(r - base), w2 = exp2_fast(r2 - base);
+            r = top;
             l = l * w1 + l2 * w2;
 #pragma unroll
             for (int k = 0; k < 8 * NB; ++k)
@@ -469,29 +547,28 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : 2) void k_attn_chunk(At
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<float2 *>(part + blk * 32 + 2 * (4 * g + i)) =
                     make_float2(o[blk][0][i], o[blk][1][i]);
-        if (g == 0) a.part_ml[head * a.splits + split] = make_float2(m, l);
+        if (g == 0) a.part_ml[head * a.splits + split] = make_float2(r, l);
         return;
     }
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t row = b * a.os.token + hq * a.os.head;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t at = row + blk * 32 + 2 * (4 * g + i);
-            const float x = o[blk][0][i] * r, y = o[blk][1][i] * r;
-            if (rt == R_F32)
+            const float x = o[blk][0][i] * inv, y = o[blk][1][i] * inv;
+            if constexpr (RT == R_F32)
                 *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(x, y);
             else
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) =
-                    rt == R_F16 ? pack2<R_F16>(x, y) : pack2<R_BF16>(x, y);
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) = pack2<RT>(x, y);
         }
-    if (a.lse && g == 0) a.lse[head] = (m == -INFINITY ? 0.0f : m / kUnit) + logf(l);
+    if (a.lse && g == 0) a.lse[head] = (r == -INFINITY ? 0.0f : r / kLog2e) + logf(l);
 }
 
 // ---------------------------------------------------------------------------
-// The chunks of a query head, one workgroup a head.  Their maxima are in the
-// first launch's units.
+// The chunks of a query head, one workgroup a head: each with its sums and the
+// reference, in log2 units, that they are relative to.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
@@ -510,7 +587,6 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(AttnArgs a, int D) {
     __syncthreads();
     m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     const float base = m == -INFINITY ? 0.0f : m;
-    const float to_log2 = a.mask ? kLog2e : 1.0f;
 
     const int row = tid / quads, quad = tid - row * quads;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -518,7 +594,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(AttnArgs a, int D) {
     if (row < rows) {
         for (int i = row; i < a.splits; i += rows) {
             const float2 x = ml[i];
-            const float w = exp2_fast((x.x - base) * to_log2);
+            const float w = exp2_fast(x.x - base);
             const float4 v = reinterpret_cast<const float4 *>(a.part + (head * a.splits + i) * D)[quad];
             l = fmaf(w, x.y, l);
             o.x = fmaf(w, v.x, o.x);
@@ -542,7 +618,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(AttnArgs a, int D) {
     const float r = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t b = head / a.Hq, h = head - b * a.Hq;
     store4<RT>(a.out, b * a.os.token + h * a.os.head + 4 * quad, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
-    if (a.lse && tid == 0) a.lse[head] = base * (to_log2 / kLog2e) + logf(l);
+    if (a.lse && tid == 0) a.lse[head] = base / kLog2e + logf(l);
 }
 
 struct AttnSplit {
@@ -554,7 +630,7 @@ static AttnSplit attn_split(int64_t B, int64_t Hq, int64_t heads, int64_t max_le
     // a window starts anywhere in a group of 16
     const int64_t span = window > 0 && window < max_len ? window + kGroup - 1 : max_len;
     const int64_t group = Hq / heads, columns = B * heads * ((group + kHeadTile - 1) / kHeadTile);
-    const int64_t want = (8 * kCUs + columns - 1) / columns;
+    const int64_t want = (2 * kCUs + columns - 1) / columns;
     int64_t chunk = (span + want - 1) / want;
     chunk = (chunk + 127) / 128 * 128;
     if (chunk < 256) chunk = 256;
@@ -575,8 +651,10 @@ static hipError_t launch_attn_f(int rt, AttnArgs a, int64_t B, void *workspace, 
     a.part = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part + B * a.Hq * s.splits * D);
     const int group = a.Hq / a.c.heads, tiles = (group + kHeadTile - 1) / kHeadTile;
-    void *args[] = {(void *)&a, (void *)&rt};
-    const void *k = a.mask ? (const void *)k_attn_chunk<F, NB, true> : (const void *)k_attn_chunk<F, NB, false>;
+    void *args[] = {(void *)&a};
+    const void *k = rt == R_F32   ? (const void *)k_attn_chunk<F, NB, R_F32>
+                    : rt == R_F16 ? (const void *)k_attn_chunk<F, NB, R_F16>
+                                  : (const void *)k_attn_chunk<F, NB, R_BF16>;
     hipError_t e = hipLaunchKernel(k, dim3((unsigned)s.splits, (unsigned)(a.c.heads * tiles), (unsigned)B),
                                    dim3(kAttnThreads), args, 0, st);
     if (e != hipSuccess || s.splits == 1) return e;
