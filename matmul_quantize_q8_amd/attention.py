@@ -74,7 +74,7 @@ def _dtype(t) -> int:
 
 def _rows(name, t, shape, dtype):
     """(address, token stride, head stride) of rows of that shape and type."""
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: want {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     token, head, one = t.stride()
     if one != 1:
@@ -86,7 +86,7 @@ def _rows(name, t, shape, dtype):
 
 def _array(name, t, dtype, shape):
     """Address of a contiguous array on the GPU."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: want a contiguous {dtype} {shape} on the GPU, got {t.dtype} {tuple(t.shape)}"
                          f" on {t.device}")
     return t.data_ptr()

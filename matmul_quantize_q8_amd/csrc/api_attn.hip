@@ -8,8 +8,8 @@
 namespace qmm {
 hipError_t launch_rope(int rt, Rope r, const void *x, void *y, const int32_t *positions, int64_t T, int H, int D,
                        Strides xs, Strides ys, hipStream_t st);
-hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, int64_t T, hipStream_t st);
-hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, int64_t T, hipStream_t st);
+hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, hipStream_t st);
+hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, hipStream_t st);
 hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, hipStream_t st);
 int64_t attn_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_len, int64_t window);
 }  // namespace qmm
@@ -102,12 +102,13 @@ qmm_status kv_write(int fmt, const qmm_rope_plan *plan, const qmm_kv_cache *cach
     a.v = v;
     a.positions = positions;
     a.slots = slots;
+    a.T = T;
     a.Hq = (int)Hq;
     a.qs = qs;
     a.qos = qos;
     a.ks = ks;
     a.vs = vs;
-    return launched(launch_kv_write(fmt, (int)(D / 32), dtype, a, T, static_cast<hipStream_t>(stream)));
+    return launched(launch_kv_write(fmt, (int)(D / 32), dtype, a, static_cast<hipStream_t>(stream)));
 }
 
 qmm_status kv_read(int fmt, const qmm_kv_cache *cache, const int64_t *slots, void *k, void *v, int dtype, int64_t T,
@@ -123,9 +124,10 @@ qmm_status kv_read(int fmt, const qmm_kv_cache *cache, const int64_t *slots, voi
     a.slots = slots;
     a.k = k;
     a.v = v;
+    a.T = T;
     a.ks = ks;
     a.vs = vs;
-    return launched(launch_kv_read(fmt, (int)(cache->dim / 32), dtype, a, T, static_cast<hipStream_t>(stream)));
+    return launched(launch_kv_read(fmt, (int)(cache->dim / 32), dtype, a, static_cast<hipStream_t>(stream)));
 }
 
 // Bytes of the workspace; 0 for sizes outside the limits.

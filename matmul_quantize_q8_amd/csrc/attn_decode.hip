@@ -55,33 +55,6 @@ __device__ __forceinline__ void split_halves(float a, float b, uint32_t &hi, uin
     split_products(a, (_Float16)1.0f, b, (_Float16)1.0f, hi, lo);
 }
 
-// Maximum / sum over the four lanes n, n + 16, n + 32, n + 48, in all of them.
-// A permlane swap exchanges the odd rows of 16 (or the upper 32 lanes) of one
-// register with the even rows (the lower 32) of the other: of two copies of x,
-// one comes back with the even row's value in both rows and the other with the
-// odd row's.  Written as instructions, with the wait that a register just
-// written needs, because the compiler's builtin yields its first result twice.
-template <bool W32>
-__device__ __forceinline__ void swap_rows(float x, float &even, float &odd) {
-    even = odd = x;
-    if constexpr (W32)
-        asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
-    else
-        asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
-}
-__device__ __forceinline__ float max_rows(float x) {
-    float a, b;
-    swap_rows<false>(x, a, b);
-    swap_rows<true>(fmaxf(a, b), a, b);
-    return fmaxf(a, b);
-}
-__device__ __forceinline__ float sum_rows(float x) {
-    float a, b;
-    swap_rows<false>(x, a, b);
-    swap_rows<true>(a + b, a, b);
-    return a + b;
-}
-
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // tanh to about 2^-22: Lambert's continued fraction, five levels deep, up to 0.6
@@ -96,11 +69,6 @@ __device__ __forceinline__ float tanh_f32(float x) {
 // ---------------------------------------------------------------------------
 // A lane's bytes of a group, and its scales
 // ---------------------------------------------------------------------------
-template <int BYTES>
-struct __attribute__((packed, aligned(BYTES))) Unit {
-    uint32_t w[BYTES / 4];
-};
-
 // A lane's L bytes of the codes at `codes`: unit u of lane i is at (64 u + i) U.
 template <int F, int NB>
 __device__ __forceinline__ void load_codes(const uint8_t *codes, int lane, uint32_t (&x)[Kv<F, NB>::L / 4]) {

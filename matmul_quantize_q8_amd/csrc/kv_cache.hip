@@ -1,6 +1,14 @@
 // The paged key-value cache: rows quantized as they are written (with the
 // rotation of queries and keys in the same launch), and read back.
 //
+// Reading, a workgroup takes 16 tokens; a wave takes the rows of one head of all 16, in
+// the lanes of the cache's byte order: for keys (and queries) lane (g, r) holds
+// of token r the values 32b + 8g + i, for values lane (g, m) holds of tokens
+// 4g + i the values 32b + 2m + e.  So 16 tokens of one aligned group, which is
+// what a prompt writes and reads, move as whole lines of the cache and as 64-byte
+// pieces of the rows; tokens with slots anywhere take the same path, each lane
+// with its own address.
+//
 // Bit-exactness: as in quantize.hip, every step of a quantizer is one correctly
 // rounded f32 operation, so a row's codes and scales are those of the weight
 // quantizers of the same format.
@@ -10,8 +18,32 @@ namespace qmm {
 
 int row_parts(int64_t T, int64_t rows, int rows_per_workgroup);
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowWaves = 4, kTokens = 16;
 
+// BYTES bytes at p (aligned to them) into words, low bytes first.
+template <int BYTES>
+__device__ __forceinline__ void load_piece(const uint8_t *p, uint32_t *w) {
+    if constexpr (BYTES == 1)
+        *w = *p;
+    else if constexpr (BYTES == 2)
+        *w = *reinterpret_cast<const uint16_t *>(p);
+    else {
+        const Unit<BYTES> u = *reinterpret_cast<const Unit<BYTES> *>(p);
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) w[i] = u.w[i];
+    }
+}
+
+// A row's NB scales.
+template <int NB>
+__device__ __forceinline__ void load_row_scales(const uint8_t *p, float (&d)[NB]) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) d[b] = f16_bits_to_f32(reinterpret_cast<const uint16_t *>(p)[b]);
+}
+
+// ---------------------------------------------------------------------------
+// Writing
+// ---------------------------------------------------------------------------
 // Codes of a block's quad (four of 32 values, eight lanes a block), one a byte
 // and offset to be unsigned; d is the block's scale.  All eight lanes call it.
 template <int F>
@@ -48,78 +80,51 @@ __device__ __forceinline__ uint32_t quad_codes(float4 v, int part, float &d) {
 template <int F, int NB>
 __device__ __forceinline__ void store_quad(uint8_t *side, int page, int t, int quad, bool values, float4 v) {
     using K = Kv<F, NB>;
-    uint8_t *grp = side + (t >> 4) * K::kGroupBytes;
+    const int b = quad >> 3, part = quad & 7, e = K::byte_of(b * 8 + (part & 1) * 4), w = K::byte_of(2 * b);
+    uint8_t *const kp = side + K::key_unit(t, part >> 1, e / K::U) + e % K::U;
+    uint8_t *const v0 = side + K::value_byte(t, 2 * part, w), *const v1 = side + K::value_byte(t, 2 * part + 1, w);
     if constexpr (F == KV_F16) {
         const uint32_t lo = pack2<R_F16>(v.x, v.y), hi = pack2<R_F16>(v.z, v.w);
         if (values) {
-            *reinterpret_cast<uint32_t *>(grp + K::value_byte(t, quad, 0)) = lo;
-            *reinterpret_cast<uint32_t *>(grp + K::value_byte(t, quad, 1)) = hi;
+            *reinterpret_cast<uint32_t *>(v0) = lo;
+            *reinterpret_cast<uint32_t *>(v1) = hi;
         } else {
-            *reinterpret_cast<uint2 *>(grp + K::key_byte(t, quad)) = make_uint2(lo, hi);
+            *reinterpret_cast<uint2 *>(kp) = make_uint2(lo, hi);
         }
     } else {
         float d;
-        const uint32_t c = quad_codes<F>(v, quad & 7, d);
+        const uint32_t c = quad_codes<F>(v, part, d);
         if constexpr (F == KV_Q8_0) {
             if (values) {
-                *reinterpret_cast<uint16_t *>(grp + K::value_byte(t, quad, 0)) = (uint16_t)c;
-                *reinterpret_cast<uint16_t *>(grp + K::value_byte(t, quad, 1)) = (uint16_t)(c >> 16);
+                *reinterpret_cast<uint16_t *>(v0) = (uint16_t)c;
+                *reinterpret_cast<uint16_t *>(v1) = (uint16_t)(c >> 16);
             } else {
-                *reinterpret_cast<uint32_t *>(grp + K::key_byte(t, quad)) = c;
+                *reinterpret_cast<uint32_t *>(kp) = c;
             }
         } else {
             const uint32_t two = c | (c >> 4);            // bytes 0 and 2: the pairs' nibbles
             if (values) {
-                grp[K::value_byte(t, quad, 0)] = (uint8_t)two;
-                grp[K::value_byte(t, quad, 1)] = (uint8_t)(two >> 16);
+                *v0 = (uint8_t)two;
+                *v1 = (uint8_t)(two >> 16);
             } else {
-                *reinterpret_cast<uint16_t *>(grp + K::key_byte(t, quad)) =
+                *reinterpret_cast<uint16_t *>(kp) =
                     (uint16_t)((two & 0xffu) | ((two >> 8) & 0xff00u));
             }
         }
-        if ((quad & 7) == 0) {
-            uint16_t *sc = reinterpret_cast<uint16_t *>(side + (page >> 4) * K::kGroupBytes);
-            sc[t * NB + (quad >> 3)] = (uint16_t)f32_to_f16_bits(d);
+        if (part == 0) {
+            *reinterpret_cast<uint16_t *>(side + K::scale_byte(page, t) + 2 * b) = (uint16_t)f32_to_f16_bits(d);
         }
     }
 }
 
-// The values of a quad.
-template <int F, int NB>
-__device__ __forceinline__ float4 load_quad(const uint8_t *side, int page, int t, int quad, bool values) {
-    using K = Kv<F, NB>;
-    const uint8_t *grp = side + (t >> 4) * K::kGroupBytes;
-    const int k0 = K::key_byte(t, quad), v0 = K::value_byte(t, quad, 0), v1 = K::value_byte(t, quad, 1);
-    if constexpr (F == KV_F16) {
-        uint32_t lo, hi;
-        if (values) {
-            lo = *reinterpret_cast<const uint32_t *>(grp + v0);
-            hi = *reinterpret_cast<const uint32_t *>(grp + v1);
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(grp + k0);
-            lo = u.x;
-            hi = u.y;
-        }
-        return make_float4(f16_bits_to_f32(lo), f16_bits_to_f32(lo >> 16), f16_bits_to_f32(hi),
-                           f16_bits_to_f32(hi >> 16));
-    } else {
-        const uint16_t *sc = reinterpret_cast<const uint16_t *>(side + (page >> 4) * K::kGroupBytes);
-        const float d = f16_bits_to_f32(sc[t * NB + (quad >> 3)]);
-        int c[4];
-        if constexpr (F == KV_Q8_0) {
-            const uint32_t u = values ? (uint32_t) * reinterpret_cast<const uint16_t *>(grp + v0) |
-                                            (uint32_t) * reinterpret_cast<const uint16_t *>(grp + v1) << 16
-                                      : *reinterpret_cast<const uint32_t *>(grp + k0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = (int)((u >> (8 * k)) & 255u) - 128;
-        } else {
-            const uint32_t u = values ? (uint32_t)grp[v0] | (uint32_t)grp[v1] << 8
-                                      : (uint32_t) * reinterpret_cast<const uint16_t *>(grp + k0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = (int)((u >> (4 * k)) & 15u) - 8;
-        }
-        return make_float4(d * (float)c[0], d * (float)c[1], d * (float)c[2], d * (float)c[3]);
-    }
+// The token of workgroup i of T.  Workgroups go to the eight XCDs in turn, each
+// with an L2 of its own; 16 consecutive tokens, which share lines of a group's
+// codes when they are written in order, are given to one of them.
+__device__ __forceinline__ int64_t token_of(int64_t i, int64_t T) {
+    constexpr int64_t n = 8 * kTokens;
+    if (i >= T / n * n) return i;
+    const int64_t j = i % n;
+    return i - j + (j % 8) * kTokens + j / 8;
 }
 
 // One workgroup a token (and part of its rows): query rows, then key rows, then
@@ -128,7 +133,7 @@ template <int F, int NB, int RT>
 __global__ __launch_bounds__(kRowThreads) void k_kv_write(WriteArgs a) {
     constexpr int kQuads = 8 * NB, kPer = 64 / kQuads;
     __shared__ float2 cs[kMaxHeadDim / 2];
-    const int64_t t = blockIdx.x;
+    const int64_t t = token_of(blockIdx.x, a.T);
     if (a.r.rot) {
         rope_table(a.r, a.positions[t], cs, threadIdx.x, kRowThreads);
         __syncthreads();
@@ -157,35 +162,95 @@ __global__ __launch_bounds__(kRowThreads) void k_kv_write(WriteArgs a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Reading
+// ---------------------------------------------------------------------------
+// Value number k of a lane's words, before its scale.
+template <int F>
+__device__ __forceinline__ float code_value(const uint32_t *w, int k) {
+    if constexpr (F == KV_F16) return f16_bits_to_f32(w[k >> 1] >> (16 * (k & 1)));
+    if constexpr (F == KV_Q8_0) return (float)((int)((w[k >> 2] >> (8 * (k & 3))) & 255u) - 128);
+    return (float)((int)((w[k >> 3] >> (4 * (k & 7))) & 15u) - 8);
+}
+
 template <int F, int NB, int RT>
 __global__ __launch_bounds__(kRowThreads) void k_kv_read(ReadArgs a) {
-    constexpr int kQuads = 8 * NB, kPer = 64 / kQuads;
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int sub = lane / kQuads, quad = lane - sub * kQuads;
-    if (sub >= kPer) return;
-    const int page = 1 << a.c.page_shift;
-    const int64_t slot = a.slots[t], pg = slot >> a.c.page_shift;
-    const bool good = a.c.has_page(pg);
-    const int at = (int)(slot & (page - 1));
-    const int64_t side = Kv<F, NB>::side_bytes(page);
-    const uint8_t *base = a.c.page_at(good ? pg : 0, side);
+    using K = Kv<F, NB>;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    const int count = (int)min((int64_t)kTokens, a.T - t0);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int g = lane >> 4, r = lane & 15, page = 1 << a.c.page_shift;
+    const int64_t side = K::side_bytes(page);
     const int H = a.c.heads, first = a.k ? 0 : H, rows = a.v ? 2 * H : H;
-    const int step = gridDim.y * (kRowThreads / 64) * kPer;
-    for (int row = first + (blockIdx.y * (kRowThreads / 64) + wave) * kPer + sub; row < rows; row += step) {
-        const bool values = row >= H;
-        const int h = row - (values ? H : 0);
-        const float nan = __builtin_bit_cast(float, 0x7fc00000u);
-        float4 y = make_float4(nan, nan, nan, nan);
-        if (good) y = load_quad<F, NB>(base + (2 * h + values) * side, page, at, quad, values);
-        const Strides s = values ? a.vs : a.ks;
-        store4<RT>(values ? a.v : a.k, t * s.token + h * s.head + 4 * quad, y);
+    const float nan = __builtin_bit_cast(float, 0x7fc00000u);
+    for (int row = first + blockIdx.y * kRowWaves + wave; row < rows; row += gridDim.y * kRowWaves) {
+        if (row < H) {
+            if (r >= count) continue;
+            const int64_t slot = a.slots[t0 + r], pg = slot >> a.c.page_shift;
+            const int at = (int)(slot & (page - 1));
+            const bool good = a.c.has_page(pg);
+            uint32_t w[K::L / 4];
+            float d[NB];
+            const uint8_t *base = a.c.page_at(good ? pg : 0, side) + 2 * row * side;
+#pragma unroll
+            for (int u = 0; u < K::NU; ++u) load_piece<K::U>(base + K::key_unit(at, g, u), w + u * (K::U / 4));
+            if constexpr (K::kScaled) load_row_scales<NB>(base + K::scale_byte(page, at), d);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = code_value<F>(w, 8 * b + i);
+                    if constexpr (K::kScaled) x[i] *= d[b];
+                    if (!good) x[i] = nan;
+                }
+                store8<RT>(a.k, (t0 + r) * a.ks.token + row * a.ks.head + 32 * b + 8 * g, x);
+            }
+        } else {
+            const int h = row - H;
+            uint32_t w[4][(K::W + 3) / 4] = {};
+            float d[4][NB];
+            bool good[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t slot = a.slots[t0 + min(4 * g + i, count - 1)], pg = slot >> a.c.page_shift;
+                const int at = (int)(slot & (page - 1));
+                good[i] = a.c.has_page(pg);
+                const uint8_t *base = a.c.page_at(good[i] ? pg : 0, side) + (2 * h + 1) * side;
+#pragma unroll
+                for (int k = 0; k < K::W; k += K::P) {
+                    uint32_t one[K::P < 4 ? 1 : K::P / 4];
+                    load_piece<K::P>(base + K::value_byte(at, r, k), one);
+                    if constexpr (K::P < 4)
+                        w[i][k >> 2] |= one[0] << (8 * (k & 3));
+                    else
+#pragma unroll
+                        for (int j = 0; j < K::P / 4; ++j) w[i][(k >> 2) + j] = one[j];
+                }
+                if constexpr (K::kScaled) load_row_scales<NB>(base + K::scale_byte(page, at), d[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (4 * g + i >= count) continue;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = code_value<F>(w[i], 2 * b + e);
+                        if constexpr (K::kScaled) x[e] *= d[i][b];
+                        if (!good[i]) x[e] = nan;
+                    }
+                    store2<RT>(a.v, (t0 + 4 * g + i) * a.vs.token + h * a.vs.head + 32 * b + 2 * r, x);
+                }
+            }
+        }
     }
 }
 
 template <int F, int NB>
-static hipError_t launch_write_f(int rt, WriteArgs a, int64_t T, hipStream_t st) {
-    const dim3 grid((unsigned)T, (unsigned)row_parts(T, a.Hq + 2 * a.c.heads, kRowThreads / 64 * (64 / (8 * NB))));
+static hipError_t launch_write_f(int rt, WriteArgs a, hipStream_t st) {
+    const dim3 grid((unsigned)a.T, (unsigned)row_parts(a.T, a.Hq + 2 * a.c.heads, kRowWaves * (64 / (8 * NB))));
     void *args[] = {(void *)&a};
     const void *k = rt == R_F32   ? (const void *)k_kv_write<F, NB, R_F32>
                     : rt == R_F16 ? (const void *)k_kv_write<F, NB, R_F16>
@@ -194,9 +259,10 @@ static hipError_t launch_write_f(int rt, WriteArgs a, int64_t T, hipStream_t st)
 }
 
 template <int F, int NB>
-static hipError_t launch_read_f(int rt, ReadArgs a, int64_t T, hipStream_t st) {
+static hipError_t launch_read_f(int rt, ReadArgs a, hipStream_t st) {
+    const int64_t groups = (a.T + kTokens - 1) / kTokens;
     const int rows = a.c.heads * ((a.k != nullptr) + (a.v != nullptr));
-    const dim3 grid((unsigned)T, (unsigned)row_parts(T, rows, kRowThreads / 64 * (64 / (8 * NB))));
+    const dim3 grid((unsigned)groups, (unsigned)row_parts(groups, rows, kRowWaves));
     void *args[] = {(void *)&a};
     const void *k = rt == R_F32   ? (const void *)k_kv_read<F, NB, R_F32>
                     : rt == R_F16 ? (const void *)k_kv_read<F, NB, R_F16>
@@ -204,12 +270,12 @@ static hipError_t launch_read_f(int rt, ReadArgs a, int64_t T, hipStream_t st) {
     return hipLaunchKernel(k, grid, dim3(kRowThreads), args, 0, st);
 }
 
-hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, int64_t T, hipStream_t st) {
-    QMM_KV_DISPATCH(launch_write_f, rt, a, T, st);
+hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, hipStream_t st) {
+    QMM_KV_DISPATCH(launch_write_f, rt, a, st);
 }
 
-hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, int64_t T, hipStream_t st) {
-    QMM_KV_DISPATCH(launch_read_f, rt, a, T, st);
+hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, hipStream_t st) {
+    QMM_KV_DISPATCH(launch_read_f, rt, a, st);
 }
 
 }  // namespace qmm

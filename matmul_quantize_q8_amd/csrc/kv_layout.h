@@ -120,6 +120,38 @@ __device__ __forceinline__ void rope_table(const Rope &r, int32_t pos, float2 *c
     }
 }
 
+// Eight consecutive values; base and i as for load4.
+template <int RT>
+__device__ __forceinline__ void load8(const void *base, int64_t i, float (&x)[8]) {
+    const float4 a = load4<RT>(base, i), b = load4<RT>(base, i + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+// Two consecutive values; i is even.
+template <int RT>
+__device__ __forceinline__ void load2(const void *base, int64_t i, float (&x)[2]) {
+    if constexpr (RT == R_F32) {
+        const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + i);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + i);
+        x[0] = RT == R_F16 ? f16_bits_to_f32(u) : __builtin_bit_cast(float, u << 16);
+        x[1] = RT == R_F16 ? f16_bits_to_f32(u >> 16) : __builtin_bit_cast(float, u & 0xffff0000u);
+    }
+}
+template <int RT>
+__device__ __forceinline__ void store2(void *base, int64_t i, const float (&x)[2]) {
+    if constexpr (RT == R_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(base) + i) = make_float2(x[0], x[1]);
+    else
+        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + i) = pack2<RT>(x[0], x[1]);
+}
+template <int RT>
+__device__ __forceinline__ void store8(void *base, int64_t i, const float (&x)[8]) {
+    store4<RT>(base, i, make_float4(x[0], x[1], x[2], x[3]));
+    store4<RT>(base, i + 4, make_float4(x[4], x[5], x[6], x[7]));
+}
+
 // Values n .. n+3 of the rotated row that starts at element `row` of `base`.
 // The pair's other value is read from memory again: the row is in the cache.
 template <int RT>
@@ -167,6 +199,47 @@ __device__ __forceinline__ float4 rotate4(const void *base, int64_t row, int n, 
 }
 
 // ---------------------------------------------------------------------------
+// Lanes of a wave as (g, r), lane = 16 g + r
+// ---------------------------------------------------------------------------
+// Maximum / sum over the four lanes n, n + 16, n + 32, n + 48, in all of them.
+// A permlane swap exchanges the odd rows of 16 (or the upper 32 lanes) of one
+// register with the even rows (the lower 32) of the other: of two copies of x,
+// one comes back with the even row's value in both rows and the other with the
+// odd row's.  Written as instructions, with the wait that a register just
+// written needs, because the compiler's builtin yields its first result twice.
+template <bool W32>
+__device__ __forceinline__ void swap_rows(float x, float &even, float &odd) {
+    even = odd = x;
+    if constexpr (W32)
+        asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
+    else
+        asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
+}
+__device__ __forceinline__ float max_rows(float x) {
+    float a, b;
+    swap_rows<false>(x, a, b);
+    swap_rows<true>(fmaxf(a, b), a, b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_rows(float x) {
+    float a, b;
+    swap_rows<false>(x, a, b);
+    swap_rows<true>(a + b, a, b);
+    return a + b;
+}
+
+// Maximum over each row of 16 lanes, in all of them.
+__device__ __forceinline__ float max16_lanes(float a) {
+    a = max8_lanes(a);
+    return fmaxf(a, dpp_f32<kDppRowRor8>(a));
+}
+
+template <int BYTES>
+struct __attribute__((packed, aligned(BYTES))) Unit {
+    uint32_t w[BYTES / 4];
+};
+
+// ---------------------------------------------------------------------------
 // The cache
 // ---------------------------------------------------------------------------
 constexpr int kGroup = 16;      // positions of a group of codes
@@ -194,14 +267,19 @@ struct Kv {
     // Byte of a lane that holds its value number v.
     __host__ __device__ static constexpr int byte_of(int v) { return v * kv_bits(F) / 8; }
 
-    // Where quad `quad` (values 4 quad .. +3) of the row of position t lies in
-    // its group.  A key's four are consecutive; a value's are two lanes' two.
-    __host__ __device__ static constexpr int key_byte(int t, int quad) {
-        return at((quad & 7) >> 1, t & 15, byte_of((quad >> 3) * 8 + (quad & 1) * 4));
+    // Where unit u of lane g of position t's key lies in a side, where byte w of
+    // lane m of its value, and where its scales.
+    __host__ __device__ static constexpr int key_unit(int t, int g, int u) {
+        return (t >> 4) * kGroupBytes + at(g, t & 15, u * U);
     }
-    __host__ __device__ static constexpr int value_byte(int t, int quad, int second) {
-        return at((t & 15) >> 2, (quad & 7) * 2 + second, byte_of((t & 3) * 2 * NB + (quad >> 3) * 2));
+    __host__ __device__ static constexpr int value_byte(int t, int m, int w) {
+        return (t >> 4) * kGroupBytes + at((t & 15) >> 2, m, (t & 3) * W + w);
     }
+    __host__ __device__ static constexpr int scale_byte(int page, int t) {
+        return (page >> 4) * kGroupBytes + t * NB * 2;
+    }
+    // Bytes of a value's W that lie together in a unit.
+    static constexpr int P = W % 16 == 0 ? 16 : W % 8 == 0 ? 8 : W % 4 == 0 ? 4 : W % 2 == 0 ? 2 : 1;
 };
 
 constexpr int64_t kv_page_bytes(int fmt, int64_t page, int64_t heads, int64_t dim) {
@@ -231,6 +309,7 @@ struct WriteArgs {
     void *qo;
     const int32_t *positions;
     const int64_t *slots;
+    int64_t T;
     int Hq;                     // 0: no queries
     Strides qs, qos, ks, vs;
 };
@@ -239,6 +318,7 @@ struct ReadArgs {
     KvCache c;
     const int64_t *slots;
     void *k, *v;                // NULL: not wanted
+    int64_t T;
     Strides ks, vs;
 };
 

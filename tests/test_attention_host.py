@@ -211,14 +211,19 @@ LAYOUT = r"""
 using namespace qmm;
 template <int F, int NB> void dump(const char *name) {
     using K = Kv<F, NB>;
+    static_assert(K::U % K::P == 0 || K::P % K::U == 0, "a value's pieces lie in one unit, or are whole units");
+    static_assert(K::P <= K::U, "a value's piece lies in one unit");
     printf("%s %d side", name, 32 * NB);
     for (int page : {16, 32, 256}) printf(" %lld", (long long)K::side_bytes(page));
     printf("\n");
-    for (int t = 0; t < 16; ++t) {
+    for (int t = 0; t < 32; ++t) {
         printf("%s %d k %d", name, 32 * NB, t);
-        for (int c = 0; c < 8 * NB; ++c) printf(" %d", K::key_byte(t, c));
+        for (int n = 0; n < 32 * NB; ++n) {
+            const int j = K::byte_of(n / 32 * 8 + n % 8);
+            printf(" %d", K::key_unit(t, n % 32 / 8, j / K::U) + j % K::U);
+        }
         printf("\n%s %d v %d", name, 32 * NB, t);
-        for (int c = 0; c < 8 * NB; ++c) printf(" %d %d", K::value_byte(t, c, 0), K::value_byte(t, c, 1));
+        for (int n = 0; n < 32 * NB; ++n) printf(" %d", K::value_byte(t, n % 32 / 2, K::byte_of(n / 32 * 2 + n % 2)));
         printf("\n");
     }
 }
@@ -260,9 +265,8 @@ def test_layout_arithmetic_of_the_kernels(tmp_path, q):
             seen += 1
             fmt, dim, values, t = w[0], int(w[1]), w[2] == "v", int(w[3])
             at, _ = code_places(fmt, dim, t, values)
-            want = at[0::2] if values else at[0::4]
-            assert [int(v) for v in w[4:]] == want.tolist(), line[:60]
-    assert seen == 3 * 5 * 32
+            assert [int(v) for v in w[4:]] == at.tolist(), line[:60]
+    assert seen == 3 * 5 * 64
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
