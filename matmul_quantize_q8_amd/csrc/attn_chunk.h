@@ -1,0 +1,631 @@
+// Attention of one new token over the paged key-value cache (include/qmm.h
+// states the formula).
+//
+// One pass over the cache with the running maximum m and sum l of the softmax.
+// The sequence is cut into chunks of positions; a workgroup takes one chunk of
+// one key head for up to 16 of its query heads, and its four waves take tiles
+// of 32 positions in turn.  A wave works alone: no LDS and no barrier until its
+// last tile.  Per tile, with matrix instructions of 16 x 16 x 32 (f16, f32 sums):
+//
+//   S[position][head] = K q   A = 16 key rows, B = the query heads; one per
+//                             block of 32 values, its result times the block's
+//                             scale, so that codes enter as small integers;
+//   O[value][head] += V^T w   A = 16 values of 32 positions, B = the weights
+//                             exp(S - m), times the positions' block scales.
+//
+// The cache's byte order makes both A operands a lane's own loaded bytes (the
+// group's lane (g, r) is the wave's lane 16 g + r), and S comes out of the
+// first in the lanes that the second needs it in, so nothing crosses lanes but
+// the maximum.  Codes are exact in f16; queries and weights enter as two f16
+// each (the value and what its rounding left: 22 bits), so a product keeps
+// f32's accuracy to 2^-21.
+//
+// The partial results of several chunks are joined by a second launch:
+//   M = max m,  l = sum l_i exp(m_i - M),  out = sum o_i exp(m_i - M) / l.
+#pragma once
+
+#include <cfloat>
+#include <type_traits>
+
+#include "kv_layout.h"
+
+namespace qmm {
+
+constexpr int kAttnThreads = 256, kAttnWaves = 4;
+constexpr int kHeadTile = 16;                   // query heads of a workgroup
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kDppRowRor4 = 0x124;              // row_ror:4: lane i of 16 reads lane (i - 4) mod 16
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// a * x and b * y as hi + lo of two f16 each, x and y f16: hi is the product
+// rounded to nearest even, lo what is left of it (one fused operation each, whose
+// f16 factors and f16 result need no conversions of their own).
+__device__ __forceinline__ void split_products(float a, _Float16 x, float b, _Float16 y, uint32_t &hi, uint32_t &lo) {
+    const v2h h = {(_Float16)fmaf((float)x, a, 0.0f), (_Float16)fmaf((float)y, b, 0.0f)};
+    const v2h l = {(_Float16)fmaf((float)x, a, -(float)h.x), (_Float16)fmaf((float)y, b, -(float)h.y)};
+    hi = __builtin_bit_cast(uint32_t, h);
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+__device__ __forceinline__ void split_halves(float a, float b, uint32_t &hi, uint32_t &lo) {
+    split_products(a, (_Float16)1.0f, b, (_Float16)1.0f, hi, lo);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// tanh to about 2^-22: Lambert's continued fraction, five levels deep, up to 0.6
+// (its first dropped part is below 1e-9 there), beyond that (e^2x - 1) / (e^2x + 1).
+__device__ __forceinline__ float tanh_f32(float x) {
+    const float y = fminf(fabsf(x), 20.0f), z = y * y, e = exp2_fast(2.0f * kLog2e * y);
+    const float num = y < 0.6f ? y * fmaf(z, fmaf(z, 21.0f, 1260.0f), 10395.0f) : e - 1.0f;
+    const float den = y < 0.6f ? fmaf(z, fmaf(z, z + 210.0f, 4725.0f), 10395.0f) : e + 1.0f;
+    return x != x ? x : copysignf(num / den, x);
+}
+
+// ---------------------------------------------------------------------------
+// A lane's bytes of a group, and its scales
+// ---------------------------------------------------------------------------
+// A lane's L bytes of the codes at `codes`: unit u of lane i is at (64 u + i) U.
+template <int F, int NB>
+__device__ __forceinline__ void load_codes(const uint8_t *codes, int lane, uint32_t (&x)[Kv<F, NB>::L / 4]) {
+    using K = Kv<F, NB>;
+#pragma unroll
+    for (int u = 0; u < K::NU; ++u) {
+        const Unit<K::U> v = *reinterpret_cast<const Unit<K::U> *>(codes + (u * 64 + lane) * K::U);
+#pragma unroll
+        for (int i = 0; i < K::U / 4; ++i) x[u * (K::U / 4) + i] = v.w[i];
+    }
+}
+
+// A wave's scales of one side of a tile, [32][NB] halves in LDS: those of
+// positions 16 j + 4 g .. + 3, two to a word.
+template <int NB>
+__device__ __forceinline__ void read_scales(const uint32_t *sc, int j, int g, uint32_t (&x)[2 * NB]) {
+    constexpr int B = NB % 2 ? 8 : 16;
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(sc + j * 8 * NB + g * 2 * NB);
+#pragma unroll
+    for (int u = 0; u < 8 * NB / B; ++u) {
+        const Unit<B> v = *reinterpret_cast<const Unit<B> *>(p + u * B);
+#pragma unroll
+        for (int i = 0; i < B / 4; ++i) x[u * (B / 4) + i] = v.w[i];
+    }
+}
+
+// Scale of position i, block b of such words.
+template <int NB>
+__device__ __forceinline__ _Float16 scale_of(const uint32_t (&x)[2 * NB], int i, int b) {
+    const int k = i * NB + b;
+    const v2h h = __builtin_bit_cast(v2h, x[k >> 1]);
+    return (k & 1) ? h.y : h.x;
+}
+
+// ---------------------------------------------------------------------------
+// Codes as operands
+// ---------------------------------------------------------------------------
+// Codes u as halves without an integer conversion: u in the low bits of a half
+// is, as f16, u * 2^-24, and one packed multiply-add makes it (u - offset) * 2^-9,
+// exactly.  (The product could take u * 2^-24 and have its accumulator start at
+// the offset's share.  That was tried, and cost accuracy: a matrix instruction
+// aligns its products by their exponent fields, so a subnormal's leading zeros
+// push out low bits.  Score errors were ten times as large with 4-bit codes.)
+template <int F> constexpr float kCodeUnit = F == KV_F16 ? 1.0f : 0x1p-9f;
+
+// Words of two codes each, at bit 0 (SHIFT = 0) or 4 of their halves.
+template <int F, int SHIFT>
+__device__ __forceinline__ uint32_t code_halves(uint32_t u) {
+    constexpr float unit = SHIFT == 4 ? 0x1p11f : 0x1p15f, offset = -(F == KV_Q8_0 ? 128.0f : 8.0f) * 0x1p-9f;
+    const v2h m = {(_Float16)unit, (_Float16)unit}, c = {(_Float16)offset, (_Float16)offset};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(v2h, u), m, c));
+}
+
+template <int F, int NB>
+__device__ __forceinline__ v4u key_operand(const uint32_t (&x)[Kv<F, NB>::L / 4], int b) {
+    v4u a;
+    if constexpr (F == KV_F16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = x[4 * b + j];
+    } else if constexpr (F == KV_Q8_0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            a[2 * j] = code_halves<F, 0>(__builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c010c00u));
+            a[2 * j + 1] = code_halves<F, 0>(__builtin_amdgcn_perm(0u, x[2 * b + j], 0x0c030c02u));
+        }
+    } else {                                    // pairs (j, j + 4): the queries are in that order too
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t y = x[b] >> (8 * j);
+            a[2 * j] = code_halves<F, 0>(y & 0x000f000fu);
+            a[2 * j + 1] = code_halves<F, 4>(y & 0x00f000f0u);
+        }
+    }
+    return a;
+}
+
+// Query slots of lane g's eight values of a block, in the key operand's order.
+template <int F>
+__device__ __forceinline__ constexpr int query_slot(int s) {
+    return F == KV_Q4_0 ? (s >> 1) + 4 * (s & 1) : s;
+}
+
+// Values 32b + 2r + e of the lane's four positions of a group, as two words of
+// two positions each.
+template <int F, int NB>
+__device__ __forceinline__ void value_words(const uint32_t (&x)[Kv<F, NB>::L / 4], int b, uint32_t (&lo)[2],
+                                            uint32_t (&hi)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {               // positions 2j, 2j + 1; lo: e = 0, hi: e = 1
+        if constexpr (F == KV_F16) {
+            const uint32_t p = x[2 * j * NB + b], q = x[(2 * j + 1) * NB + b];
+            lo[j] = __builtin_amdgcn_perm(q, p, 0x05040100u);
+            hi[j] = __builtin_amdgcn_perm(q, p, 0x07060302u);
+        } else {
+            constexpr int W = F == KV_Q8_0 ? 2 * NB : NB;
+            const int kp = 2 * j * W + (F == KV_Q8_0 ? 2 * b : b), kq = kp + W;
+            const uint32_t p = x[kp >> 2], q = x[kq >> 2];
+            const uint32_t sel = 0x0c040c00u + (uint32_t)(kp & 3) + ((uint32_t)(kq & 3) << 16);
+            const uint32_t u = __builtin_amdgcn_perm(q, p, sel);
+            if constexpr (F == KV_Q8_0) {
+                const uint32_t v = __builtin_amdgcn_perm(q, p, sel + 0x00010001u);
+                lo[j] = code_halves<F, 0>(u);
+                hi[j] = code_halves<F, 0>(v);
+            } else {
+                lo[j] = code_halves<F, 0>(u & 0x000f000fu);
+                hi[j] = code_halves<F, 4>(u & 0x00f000f0u);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One chunk
+// ---------------------------------------------------------------------------
+// Scores are kept in log2 units.  A wave's weights are 2^(s - r) for a reference
+// r that lies kWeightBits under the largest score it was set by.  The reference is moved (which
+// multiplies every accumulator) only when a score passes that one by kSlackBits:
+// weights, times value scales below 2, stay inside f16 (2^(8 + 6 + 1) = 32 768),
+// and small ones keep their low parts out of its subnormals.  Tiles with a value
+// scale of 2 and more (values beyond 254) make the wave keep r at the maximum.
+constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f;
+
+// Query heads of a key head fill the 16 columns of the score product only when
+// there are more than eight.  With fewer, COLS = 2 or 4 groups of positions share
+// the columns: head h of group c is column c * 16/COLS + h.  The products of all
+// groups go into one accumulator, each with the queries in its own columns and
+// zeros in the others, so scales, softmax and weights, the work per score, is
+// done on full columns.  For the values' product the weights are masked to their
+// group's columns again; the columns of a head are added up at the end.
+constexpr int attn_cols(int group) { return group <= 4 ? 4 : group <= 8 ? 2 : 1; }
+// Groups in a tile.
+constexpr int attn_groups(int cols) { return cols == 4 ? 4 : 2; }
+
+template <int F, int NB, int RT, int COLS>
+__global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : NB == 6 ? 2 : 3) void k_attn_chunk(AttnArgs a) {
+    using K = Kv<F, NB>;
+    constexpr int D = 32 * NB, LW = K::L / 4;
+    constexpr bool kScaled = K::kScaled;
+    constexpr int GR = attn_groups(COLS), kTile = GR * kGroup, HC = 16 / COLS, NS = GR / COLS;
+    static_assert(kScaled || COLS == 1, "an f16 cache's values are dropped by the lane that weighs them");
+    // Rows of 16 bits are exact in one f16 once scaled (what an f16's subnormals
+    // take from the smallest of them is 2^-32 of the largest), so only f32 queries
+    // need their low parts.  (Weights keep theirs for results of every type: where
+    // the values cancel, 2^-12 of a weight is more than a bf16 result's rounding.)
+    constexpr int kQueryParts = RT == R_F32 ? 2 : 1;
+    constexpr int SW = 8 * NB * GR, SR = (SW + 63) / 64;  // words of a side's scales of a tile, and of a lane
+    constexpr int QE = COLS == 1 ? 64 : 4 * HC + 1;       // entries of a block's queries: (g, head), and one of zeros
+    __shared__ float join[2 * (8 * NB + 2) * 64];
+    __shared__ v4u queries[kQueryParts][NB][QE];
+    __shared__ __attribute__((aligned(16))) uint32_t scales[kScaled ? kAttnWaves : 1][kScaled ? SW : 4];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4, c = n / HC;
+    const int group = a.Hq / a.c.heads, tiles = COLS > 1 ? 1 : (group + kHeadTile - 1) / kHeadTile;
+    const int kv = blockIdx.y / tiles, h0 = (blockIdx.y - kv * tiles) * kHeadTile, h = h0 + n % HC;
+    const int b = blockIdx.z, split = blockIdx.x;
+    const bool live = h < group;
+    const int hq = kv * group + (live ? h : h0);
+
+    float4 qx[NB][2];
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k)
+        qx[k >> 1][k & 1] = load4<RT>(a.q, b * a.qs.token + hq * a.qs.head + (k >> 1) * 32 + g * 8 + (k & 1) * 4);
+
+    const int len = a.lens[b], shift = a.c.page_shift, page = 1 << shift;
+    const bool bad_len = len < 0 || len > a.max_len;
+    const int lo = a.window && !bad_len ? max(0, len - a.window) : 0;
+    const int from = (lo & ~(kGroup - 1)) + split * a.chunk;
+    const int to = bad_len ? from : from + min(len - from, a.chunk);
+    const int64_t side = K::side_bytes(page);
+
+    // Tiles wave, wave + 4, ... of the chunk.  A tile's keys are loaded as soon as
+    // the last tile's are used up, and its values likewise, into the same
+    // registers: the loads have the other half of a tile's work to arrive in.
+    const int ntiles = (to - from + kTile - 1) / kTile;
+    int pages = 0;                              // lane i: the page of the i-th group of this wave's next 64 / GR tiles
+    const uint8_t *kside[GR];                   // the tile's groups: keys' side of the page and place in it
+    int place[GR];
+    bool bad = false;
+    uint32_t kx[GR][LW], vx[GR][LW], ks[SR], vs[SR];
+    const auto look_up = [&](int tile) {
+        const int t = from + (tile + lane / GR * kAttnWaves) * kTile + lane % GR * kGroup;
+        pages = t < to ? a.pages[b * a.pages_stride + (t >> shift)] : 0;
+    };
+    const auto locate = [&](int tile, int count) {
+        if (count > 0 && count % (64 / GR) == 0) {
+            look_up(tile);
+            asm volatile("" : "+v"(pages));     // waited for here, not at every tile's readlane
+        }
+        bad = false;
+#pragma unroll
+        for (int j = 0; j < GR; ++j) {
+            // a group past the end is not looked up: the first is read again and not used
+            const int t0 = from + tile * kTile, t = t0 + j * kGroup < to ? t0 + j * kGroup : t0;
+            int p = __builtin_amdgcn_readlane(pages, GR * (count % (64 / GR)) + (t != t0 ? j : 0));
+            if (!a.c.has_page(p)) {
+                bad = true;
+                p = 0;
+            }
+            kside[j] = a.c.page_at(p, side) + 2 * kv * side;
+            place[j] = t & (page - 1);
+        }
+    };
+    const auto load = [&](bool values, uint32_t(&x)[GR][LW], uint32_t(&sc)[SR]) {
+        const int64_t off = values ? side : 0;
+#pragma unroll
+        for (int j = 0; j < GR; ++j)
+            load_codes<F, NB>(kside[j] + off + (place[j] >> 4) * K::kGroupBytes, lane, x[j]);
+        if constexpr (kScaled) {
+#pragma unroll
+            for (int k = 0; k < SR; ++k) {
+                const int i = lane + 64 * k, j = i / (8 * NB);
+                const uint8_t *p = kside[0] + off + K::scale_byte(page, place[0]);
+#pragma unroll
+                for (int m = 1; m < GR; ++m)
+                    if (j == m) p = kside[m] + off + K::scale_byte(page, place[m]);
+                if (SW % 64 == 0 || i < SW) sc[k] = *reinterpret_cast<const uint32_t *>(p + 4 * (i - j * 8 * NB));
+            }
+        }
+    };
+    uint32_t *const sc = scales[kScaled ? wave : 0];
+    const auto stage = [&](const uint32_t(&x)[SR]) {
+#pragma unroll
+        for (int k = 0; k < SR; ++k)
+            if (SW % 64 == 0 || lane + 64 * k < SW) sc[lane + 64 * k] = x[k];
+        __builtin_amdgcn_wave_barrier();
+    };
+    look_up(wave);
+    asm volatile("" : "+v"(pages));             // and the queries with them: no wait for them reaches past the tile's loads
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) asm volatile("" : "+v"(qx[k >> 1][k & 1].x));
+    if (wave < ntiles) {
+        locate(wave, 0);
+        load(false, kx, ks);
+        load(true, vx, vs);
+    }
+
+    // The queries: scaled by a power of two to below 2^8, split in two f16, in LDS.
+    float unit;
+    {
+        float x[NB][8], top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k) {
+            const float4 v = qx[k >> 1][k & 1];
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[k >> 1][(k & 1) * 4 + i] = live ? f[i] : 0.0f;
+                top = fmaxf(top, live ? fabsf(f[i]) : 0.0f);
+            }
+        }
+        top = max_rows(top);
+        const int e = top > 0.0f && top < INFINITY ? min(max(7 - ilogbf(top), -120), 120) : 0;
+        const float up = ldexpf(1.0f, e);
+        unit = ldexpf(a.scale, -e) / kCodeUnit<F>;    // of the products: the score's natural units
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            if ((blk & (kAttnWaves - 1)) != wave) continue;   // every wave has them all and writes its share
+            v4u part[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hi, lw;
+                split_halves(x[blk][query_slot<F>(2 * j)] * up, x[blk][query_slot<F>(2 * j + 1)] * up, hi, lw);
+                part[0][j] = hi;
+                part[1][j] = lw;
+            }
+#pragma unroll
+            for (int k = 0; k < kQueryParts; ++k) {
+                if (c == 0) queries[k][blk][g * HC + n % HC] = part[k];
+                if (COLS > 1 && lane == 0) queries[k][blk][QE - 1] = v4u{0, 0, 0, 0};
+            }
+        }
+    }
+    __syncthreads();
+    int qat[COLS];                              // this lane's entry in the product of group j (mod COLS)
+    uint32_t mine[COLS];                        // all ones where the lane's column is of that group
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) {
+        qat[j] = c == j ? g * HC + n % HC : QE - 1;
+        mine[j] = c == j ? 0xffffffffu : 0u;
+    }
+
+    v4f o[NB][2];
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) o[blk][0] = o[blk][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    float r = -INFINITY, l = 0.0f, under = kWeightBits, most = kWeightBits + kSlackBits;
+
+    const float capped = a.softcap > 0.0f ? unit / a.softcap : 0.0f;
+    int count = 0;
+    const auto step = [&](int tile, auto last) {
+        constexpr bool more = !decltype(last)::value;
+        const int t0 = from + tile * kTile;
+        const bool was_bad = bad;
+        ++count;
+
+        // scores of positions t0 + 16 (COLS j + c) + 4 g + i
+        float s[NS][4];
+        if constexpr (kScaled) stage(ks);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            uint32_t kd[2 * NB];
+            if constexpr (kScaled) read_scales<NB>(sc, COLS * j + c, g, kd);
+            v4f z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+                v4f acc = kScaled ? v4f{0.f, 0.f, 0.f, 0.f} : z;
+#pragma unroll
+                for (int m = 0; m < COLS; ++m) {
+                    const v4u key = key_operand<F, NB>(kx[COLS * j + m], blk);
+#pragma unroll
+                    for (int k = 0; k < kQueryParts; ++k) acc = mfma(key, queries[k][blk][qat[m]], acc);
+                }
+                if constexpr (kScaled) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = fmaf((float)scale_of<NB>(kd, i, blk), acc[i], z[i]);
+                } else {
+                    z = acc;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = z[i];
+        }
+        if constexpr (more) {
+            locate(tile + kAttnWaves, count);
+            load(false, kx, ks);
+        }
+        if (a.softcap > 0.0f) {
+#pragma unroll
+            for (int k = 0; k < 4 * NS; ++k)
+                s[k >> 2][k & 3] = a.softcap * kLog2e * tanh_f32(s[k >> 2][k & 3] * capped);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] *= unit * kLog2e;
+        }
+        if (was_bad) {
+#pragma unroll
+            for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] = NAN;
+        }
+        if (a.mask || t0 < lo || t0 + kTile > to) {   // some positions may not be seen: whatever they hold is dropped
+            const auto extra = [&](int t) {           // what the mask adds; -inf: not seen
+                if (t < lo || t >= to) return -INFINITY;
+                if (!a.mask) return 0.0f;
+                const float x = a.mask[b * a.mask_stride + t];
+                return x == -INFINITY ? x : fmaxf(x * kLog2e, -FLT_MAX);
+            };
+#pragma unroll
+            for (int k = 0; k < 4 * NS; ++k) {
+                const int j = k >> 2, i = k & 3;
+                const float x = extra(t0 + (COLS * j + c) * kGroup + 4 * g + i);
+                s[j][i] = x == -INFINITY ? -INFINITY : s[j][i] + x;
+                if constexpr (!kScaled) {
+#pragma unroll
+                    for (int blk = 0; blk < NB; ++blk)
+                        if (x == -INFINITY) vx[j][i * NB + blk] = 0u;
+                }
+            }
+            if constexpr (kScaled) {                  // codes are finite, scales need not be
+#pragma unroll
+                for (int k = 0; k < SR; ++k) {
+                    const int e = 2 * (lane + 64 * k);
+                    if (extra(t0 + e / NB) == -INFINITY) vs[k] &= 0xffff0000u;
+                    if (extra(t0 + (e + 1) / NB) == -INFINITY) vs[k] &= 0x0000ffffu;
+                }
+            }
+        }
+
+        if constexpr (kScaled) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < SR; ++k)
+                if (SW % 64 == 0 || lane + 64 * k < SW) any |= vs[k];
+            if (__any((any & 0x40004000u) != 0)) under = most = 0.0f;
+            stage(vs);
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int k = 1; k < 4 * NS; ++k) top = fmaxf(top, s[k >> 2][k & 3]);
+        top = max_rows(top);
+        if (__any(top > r + most)) {
+            const float next = fmaxf(r, top - under);
+            const float alpha = r == next ? 1.0f : exp2_fast(r - next);
+            r = next;
+            l *= alpha;
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[blk][0][i] *= alpha;
+                    o[blk][1][i] *= alpha;
+                }
+        }
+        const float base = r == -INFINITY ? 0.0f : r;
+        float p[NS][4];
+#pragma unroll
+        for (int k = 0; k < 4 * NS; ++k) {
+            p[k >> 2][k & 3] = exp2_fast(s[k >> 2][k & 3] - base);
+            l += p[k >> 2][k & 3];
+        }
+        uint32_t vd[NS][2 * NB];
+        if constexpr (kScaled) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j) read_scales<NB>(sc, COLS * j + c, g, vd[j]);
+        }
+        uint32_t wh[NS][2], wl[NS][2];          // the weights, two positions a word
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            if (kScaled || blk == 0) {
+#pragma unroll
+                for (int k = 0; k < 2 * NS; ++k) {
+                    const int j = k >> 1, i = 2 * (k & 1);
+                    const _Float16 one = (_Float16)1.0f;
+                    split_products(p[j][i], kScaled ? scale_of<NB>(vd[j], i, blk) : one, p[j][i + 1],
+                                   kScaled ? scale_of<NB>(vd[j], i + 1, blk) : one, wh[j][k & 1], wl[j][k & 1]);
+                }
+            }
+#pragma unroll
+            for (int pair = 0; pair < GR / 2; ++pair) {   // two groups of positions to a product
+                uint32_t e0[2][2], e1[2][2];
+                value_words<F, NB>(vx[2 * pair], blk, e0[0], e1[0]);
+                value_words<F, NB>(vx[2 * pair + 1], blk, e0[1], e1[1]);
+                const v4u va = {e0[0][0], e0[0][1], e0[1][0], e0[1][1]};
+                const v4u vb = {e1[0][0], e1[0][1], e1[1][0], e1[1][1]};
+                const auto weights = [&](const uint32_t(&w)[NS][2]) {
+                    if constexpr (COLS == 1) return v4u{w[0][0], w[0][1], w[NS - 1][0], w[NS - 1][1]};
+                    const uint32_t m0 = mine[(2 * pair) % COLS], m1 = mine[(2 * pair + 1) % COLS];
+                    return v4u{w[0][0] & m0, w[0][1] & m0, w[0][0] & m1, w[0][1] & m1};
+                };
+                const v4u high = weights(wh), low = weights(wl);
+                o[blk][0] = mfma(va, high, o[blk][0]);
+                o[blk][1] = mfma(vb, high, o[blk][1]);
+                o[blk][0] = mfma(va, low, o[blk][0]);
+                o[blk][1] = mfma(vb, low, o[blk][1]);
+            }
+        }
+        if constexpr (more) load(true, vx, vs);
+    };
+    // The last tile is a call of its own: with one loop and a condition on the
+    // loads, every tile waits for all of them.
+    int tile = wave;
+    for (; tile + kAttnWaves < ntiles; tile += kAttnWaves) step(tile, std::false_type{});
+    if (tile < ntiles) step(tile, std::true_type{});
+
+    // The wave's result, then the four waves' in a fixed order: 0 + 2, 1 + 3, both.
+    l = sum_rows(l);
+    if constexpr (kScaled) {
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[blk][0][i] *= 1.0f / kCodeUnit<F>;
+                o[blk][1][i] *= 1.0f / kCodeUnit<F>;
+            }
+    }
+    if constexpr (COLS > 1) {                   // a head's columns: 8 lanes apart, and 4
+        const auto fold = [&](auto dpp) {
+            constexpr int kCtrl = decltype(dpp)::value;
+            const float r2 = dpp_f32<kCtrl>(r), l2 = dpp_f32<kCtrl>(l), top = fmaxf(r, r2);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float w1 = exp2_fast(r - base), w2 = exp2_fast(r2 - base);
+            r = top;
+            l = l * w1 + l2 * w2;
+#pragma unroll
+            for (int k = 0; k < 8 * NB; ++k) {
+                const float x = o[k >> 3][(k >> 2) & 1][k & 3];
+                o[k >> 3][(k >> 2) & 1][k & 3] = x * w1 + dpp_f32<kCtrl>(x) * w2;
+            }
+        };
+        fold(std::integral_constant<int, kDppRowRor8>{});
+        if constexpr (COLS == 4) fold(std::integral_constant<int, kDppRowRor4>{});
+    }
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1) {
+        float *slot = join + (wave & (step - 1)) * (8 * NB + 2) * 64 + lane;
+        if (step == 1) __syncthreads();
+        if (wave >= step && wave < 2 * step) {
+            slot[0] = r;
+            slot[64] = l;
+#pragma unroll
+            for (int k = 0; k < 8 * NB; ++k) slot[(2 + k) * 64] = o[k >> 3][(k >> 2) & 1][k & 3];
+        }
+        __syncthreads();
+        if (wave < step) {
+            const float r2 = slot[0], l2 = slot[64], top = fmaxf(r, r2);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float w1 = exp2_fast(r - base), w2 = exp2_fast(r2 - base);
+            r = top;
+            l = l * w1 + l2 * w2;
+#pragma unroll
+            for (int k = 0; k < 8 * NB; ++k)
+                o[k >> 3][(k >> 2) & 1][k & 3] = o[k >> 3][(k >> 2) & 1][k & 3] * w1 + slot[(2 + k) * 64] * w2;
+        }
+    }
+    if (wave != 0 || !live || c != 0) return;
+    if (bad_len) l = NAN;
+    const int64_t head = (int64_t)b * a.Hq + hq;
+    if (a.splits > 1) {
+        float *part = a.part + (head * a.splits + split) * D;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float2 *>(part + blk * 32 + 2 * (4 * g + i)) =
+                    make_float2(o[blk][0][i], o[blk][1][i]);
+        if (g == 0) a.part_ml[head * a.splits + split] = make_float2(r, l);
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t row = b * a.os.token + hq * a.os.head;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = row + blk * 32 + 2 * (4 * g + i);
+            const float x = o[blk][0][i] * inv, y = o[blk][1][i] * inv;
+            if constexpr (RT == R_F32)
+                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(x, y);
+            else
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) = pack2<RT>(x, y);
+        }
+    if (a.lse && g == 0) a.lse[head] = (r == -INFINITY ? 0.0f : r / kLog2e) + logf(l);
+}
+
+// The first launch of a format, for the query heads of a key head that decide the columns.
+template <int F, int NB, int COLS>
+hipError_t launch_chunks_c(int rt, AttnArgs a, int64_t B, hipStream_t st) {
+    const int group = a.Hq / a.c.heads, tiles = COLS > 1 ? 1 : (group + kHeadTile - 1) / kHeadTile;
+    void *args[] = {(void *)&a};
+    const void *k = rt == R_F32   ? (const void *)k_attn_chunk<F, NB, R_F32, COLS>
+                    : rt == R_F16 ? (const void *)k_attn_chunk<F, NB, R_F16, COLS>
+                                  : (const void *)k_attn_chunk<F, NB, R_BF16, COLS>;
+    return hipLaunchKernel(k, dim3((unsigned)a.splits, (unsigned)(a.c.heads * tiles), (unsigned)B),
+                           dim3(kAttnThreads), args, 0, st);
+}
+
+template <int F, int NB>
+hipError_t launch_chunks_f(int rt, AttnArgs a, int64_t B, hipStream_t st) {
+    if constexpr (F != KV_F16) {
+        const int cols = attn_cols(a.Hq / a.c.heads);
+        if (cols == 4) return launch_chunks_c<F, NB, 4>(rt, a, B, st);
+        if (cols == 2) return launch_chunks_c<F, NB, 2>(rt, a, B, st);
+    }
+    return launch_chunks_c<F, NB, 1>(rt, a, B, st);
+}
+
+template <int F>
+hipError_t launch_chunks(int nb, int rt, const AttnArgs &a, int64_t B, hipStream_t st) {
+    switch (nb) {
+        case 2: return launch_chunks_f<F, 2>(rt, a, B, st);
+        case 3: return launch_chunks_f<F, 3>(rt, a, B, st);
+        case 4: return launch_chunks_f<F, 4>(rt, a, B, st);
+        case 6: return launch_chunks_f<F, 6>(rt, a, B, st);
+        case 8: return launch_chunks_f<F, 8>(rt, a, B, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace qmm
