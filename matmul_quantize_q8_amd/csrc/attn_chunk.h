@@ -202,15 +202,20 @@ constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f;
 // done on full columns.  For the values' product the weights are masked to their
 // group's columns again; the columns of a head are added up at the end.
 constexpr int attn_cols(int group) { return group <= 4 ? 4 : group <= 8 ? 2 : 1; }
-// Groups in a tile.
-constexpr int attn_groups(int cols) { return cols == 4 ? 4 : 2; }
+
+// A lane's bytes of four groups fit its registers beside the accumulators.
+template <int F, int NB> constexpr bool kFourColumns = Kv<F, NB>::L <= 48;
+// Groups of 16 positions in a wave's tile.
+template <int F, int NB, int COLS>
+constexpr int kTileGroups = COLS == 4 || Kv<F, NB>::L <= (COLS == 2 ? 24 : NB <= 3 ? 16 : 0) ? 4 : 2;
 
 template <int F, int NB, int RT, int COLS>
-__global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : NB == 6 ? 2 : 3) void k_attn_chunk(AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F32) ? 1 : NB >= 6 ? 2 : 3) void k_attn_chunk(AttnArgs a) {
     using K = Kv<F, NB>;
     constexpr int D = 32 * NB, LW = K::L / 4;
     constexpr bool kScaled = K::kScaled;
-    constexpr int GR = attn_groups(COLS), kTile = GR * kGroup, HC = 16 / COLS, NS = GR / COLS;
+    constexpr int GR = kTileGroups<F, NB, COLS>, kTile = GR * kGroup, HC = 16 / COLS, NS = GR / COLS;
+    static_assert(COLS <= GR, "");
     static_assert(kScaled || COLS == 1, "an f16 cache's values are dropped by the lane that weighs them");
     // Rows of 16 bits are exact in one f16 once scaled (what an f16's subnormals
     // take from the smallest of them is 2^-32 of the largest), so only f32 queries
@@ -286,7 +291,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : NB == 6 ? 2 : 3) void k
                 const int i = lane + 64 * k, j = i / (8 * NB);
                 const uint8_t *p = kside[0] + off + K::scale_byte(page, place[0]);
 #pragma unroll
-                for (int m = 1; m < GR; ++m)
+                for (int m = 64 * k / (8 * NB); m < GR && m <= (64 * k + 63) / (8 * NB); ++m)
                     if (j == m) p = kside[m] + off + K::scale_byte(page, place[m]);
                 if (SW % 64 == 0 || i < SW) sc[k] = *reinterpret_cast<const uint32_t *>(p + 4 * (i - j * 8 * NB));
             }
@@ -495,9 +500,10 @@ __global__ __launch_bounds__(kAttnThreads, NB == 8 ? 1 : NB == 6 ? 2 : 3) void k
                 const v4u va = {e0[0][0], e0[0][1], e0[1][0], e0[1][1]};
                 const v4u vb = {e1[0][0], e1[0][1], e1[1][0], e1[1][1]};
                 const auto weights = [&](const uint32_t(&w)[NS][2]) {
-                    if constexpr (COLS == 1) return v4u{w[0][0], w[0][1], w[NS - 1][0], w[NS - 1][1]};
+                    const int j0 = 2 * pair / COLS, j1 = (2 * pair + 1) / COLS;
+                    if constexpr (COLS == 1) return v4u{w[j0][0], w[j0][1], w[j1][0], w[j1][1]};
                     const uint32_t m0 = mine[(2 * pair) % COLS], m1 = mine[(2 * pair + 1) % COLS];
-                    return v4u{w[0][0] & m0, w[0][1] & m0, w[0][0] & m1, w[0][1] & m1};
+                    return v4u{w[j0][0] & m0, w[j0][1] & m0, w[j1][0] & m1, w[j1][1] & m1};
                 };
                 const v4u high = weights(wh), low = weights(wl);
                 o[blk][0] = mfma(va, high, o[blk][0]);
@@ -610,8 +616,9 @@ template <int F, int NB>
 hipError_t launch_chunks_f(int rt, AttnArgs a, int64_t B, hipStream_t st) {
     if constexpr (F != KV_F16) {
         const int cols = attn_cols(a.Hq / a.c.heads);
-        if (cols == 4) return launch_chunks_c<F, NB, 4>(rt, a, B, st);
-        if (cols == 2) return launch_chunks_c<F, NB, 2>(rt, a, B, st);
+        if constexpr (kFourColumns<F, NB>)
+            if (cols == 4) return launch_chunks_c<F, NB, 4>(rt, a, B, st);
+        if (cols >= 2) return launch_chunks_c<F, NB, 2>(rt, a, B, st);
     }
     return launch_chunks_c<F, NB, 1>(rt, a, B, st);
 }
