@@ -20,8 +20,7 @@
 // each (the value and what its rounding left: 22 bits), so a product keeps
 // f32's accuracy to 2^-21.
 //
-// The partial results of several chunks are joined by a second launch:
-//   M = max m,  l = sum l_i exp(m_i - M),  out = sum o_i exp(m_i - M) / l.
+// The partial results of several chunks are joined by a second launch (attn_decode.hip).
 #pragma once
 
 #include <cfloat>
@@ -57,6 +56,7 @@ __device__ __forceinline__ void split_products(float a, _Float16 x, float b, _Fl
 __device__ __forceinline__ void split_halves(float a, float b, uint32_t &hi, uint32_t &lo) {
     split_products(a, (_Float16)1.0f, b, (_Float16)1.0f, hi, lo);
 }
+
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -590,12 +590,8 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t at = row + blk * 32 + 2 * (4 * g + i);
-            const float x = o[blk][0][i] * inv, y = o[blk][1][i] * inv;
-            if constexpr (RT == R_F32)
-                *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(x, y);
-            else
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) = pack2<RT>(x, y);
+            const float x[2] = {o[blk][0][i] * inv, o[blk][1][i] * inv};
+            store2<RT>(a.out, row + blk * 32 + 2 * (4 * g + i), x);
         }
     if (a.lse && g == 0) a.lse[head] = (r == -INFINITY ? 0.0f : r / kLog2e) + logf(l);
 }

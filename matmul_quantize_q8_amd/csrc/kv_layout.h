@@ -332,7 +332,7 @@ struct AttnArgs {
     int64_t mask_stride;
     float *lse;                 // NULL: not wanted
     float *part;                // [B * Hq][splits][D] partial sums
-    float2 *part_ml;            // [B * Hq][splits] their maximum and sum of weights
+    float2 *part_ml;            // [B * Hq][splits] their reference and sum of weights
     int Hq, max_len, window, splits, chunk;
     float scale, softcap;
     Strides qs, os;

@@ -132,6 +132,19 @@ def test_workspace_that_is_a_byte_short(q):
     assert attn(q.lib(), "q8_0", ws_bytes=need - 1) == 1
 
 
+def test_workspace_grows_with_batch_and_length(q):
+    """What suffices for a batch and a length suffices for smaller ones."""
+    size = q.qmm_attn_decode_workspace
+    for Hq, heads, dim in ((32, 8, 128), (32, 32, 64), (64, 1, 256), (20, 1, 96)):
+        for n in (1, 255, 256, 257, 4096, 131072):
+            of = [size(B, Hq, heads, dim, n) for B in range(1, 600, 7)]
+            assert of == sorted(of)
+        for B in (1, 3, 64, 511):
+            of = [size(B, Hq, heads, dim, n) for n in range(1, 20000, 97)]
+            assert of == sorted(of)
+            assert size(B, Hq, heads, dim, 5000, 300) <= size(B, Hq, heads, dim, 5000)
+
+
 @pytest.mark.parametrize("args", [(0, 4, 2, 64, 256), (2, 3, 2, 64, 256), (2, 4, 0, 64, 256), (2, 4, 2, 65, 256),
                                   (2, 4, 2, 64, 0), (2, 4, 2, 64, 1 << 31), (2, 4, 2, 64, 256, -1)])
 def test_no_workspace_for_sizes_outside_the_limits(q, args):

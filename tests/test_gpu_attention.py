@@ -499,6 +499,28 @@ def test_attention_repeats_strides_streams(env, fmt):
     assert bool((out[..., 128:] == 3.0).all())
 
 
+def test_workspace_serves_other_sizes(env):
+    """One workspace, calls of different batches, lengths and splits in turn: each
+    gives the bits it gives on a workspace of its own."""
+    torch, q, _ = env
+    _say("workspace reuse")
+    setups = [Setup(env, "q8_0", lens, 8, 2, 64, 16, "f32", i) for i, lens in enumerate(
+        [[900] * 3, [3000], [17, 2000] * 20, [5000, 100], [300] * 40, [1500] * 7])]
+    own = []
+    for s in setups:
+        s.run()
+        own.append((s.out.clone(), s.lse.clone()))
+        s.check()
+    shared = q.attn_workspace(40, 8, 2, 64, 5000)
+    for _ in range(2):
+        for s, (out, lse) in zip(setups, own):
+            assert q.qmm_attn_decode_workspace(len(s.lens), 8, 2, 64, s.max_len) <= shared.numel()
+            s.ws = shared
+            s.out.fill_(float("nan"))
+            s.run()
+            assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_step_in_a_graph(env, fmt):
     """A decode step (rotate, write, attend) captured once, replayed at growing
