@@ -617,3 +617,22 @@ def test_binding_refusals(env):
         q.qmm_kv_write_q8_0(s.q, s.q, s.cache, torch.zeros(1, dtype=torch.int64, device="cuda"))   # 4 heads, not 2
     with pytest.raises(ValueError):
         q.qmm_kv_read_q8_0(s.cache, torch.zeros(1, dtype=torch.int64, device="cuda"), None, None)
+
+
+@pytest.mark.parametrize("cache", FORMATS)
+@pytest.mark.parametrize("weights", ["q4_0", "q8_0", "q4_k"])
+def test_attention_block_example(env, cache, weights, monkeypatch, capsys):
+    """The example runs matvec, rotation, cache and attention together and checks itself."""
+    import importlib.util
+    import os
+    import sys
+    _say("example", cache, weights)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("attention_decode", os.path.join(root, "examples",
+                                                                                   "attention_decode.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    monkeypatch.setattr(sys, "argv", ["attention_decode", "--tokens", "9", "--prompt", "39", "--cache", cache,
+                                      "--weights", weights])
+    assert example.main() == 0
+    assert "us a step" in capsys.readouterr().out
