@@ -10,7 +10,8 @@ hipError_t launch_rope(int rt, Rope r, const void *x, void *y, const int32_t *po
                        Strides xs, Strides ys, hipStream_t st);
 hipError_t launch_kv_write(int fmt, int nb, int rt, WriteArgs a, hipStream_t st);
 hipError_t launch_kv_read(int fmt, int nb, int rt, ReadArgs a, hipStream_t st);
-hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, hipStream_t st);
+hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, int64_t workspace_bytes,
+                       hipStream_t st);
 int64_t attn_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_len, int64_t window);
 }  // namespace qmm
 
@@ -172,7 +173,8 @@ qmm_status attn_decode(int fmt, const qmm_kv_cache *cache, const void *q, void *
     a.softcap = softcap;
     a.qs = qs;
     a.os = os;
-    return launched(launch_attn(fmt, (int)(cache->dim / 32), dtype, a, B, workspace, static_cast<hipStream_t>(stream)));
+    return launched(launch_attn(fmt, (int)(cache->dim / 32), dtype, a, B, workspace, ws_bytes,
+                                static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

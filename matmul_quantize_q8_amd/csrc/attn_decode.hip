@@ -108,15 +108,19 @@ static AttnSplit attn_split(int64_t B, int64_t Hq, int64_t heads, int64_t max_le
 // over every smaller batch and length too, which may be split further: a batch of
 // B has at most B + kSplitColumns / (columns of a sequence) chunks for each of a
 // sequence's columns, and at most one for kMinChunk positions.
+static int64_t part_bytes(int64_t B, int64_t Hq, int64_t splits, int64_t D) { return B * Hq * splits * (D + 2) * 4; }
+
 int64_t attn_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_len, int64_t window) {
     const int64_t per = head_tiles(Hq, heads), span = attn_span(max_len, window);
     const int64_t by_columns = B + (kSplitColumns + per - 1) / per, by_length = B * ((span + kMinChunk - 1) / kMinChunk);
     return (by_columns < by_length ? by_columns : by_length) * Hq * (D + 2) * 4;
 }
 
-hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, hipStream_t st) {
+hipError_t launch_attn(int fmt, int nb, int rt, AttnArgs a, int64_t B, void *workspace, int64_t workspace_bytes,
+                       hipStream_t st) {
     const AttnSplit s = attn_split(B, a.Hq, a.c.heads, a.max_len, a.window);
     int D = 32 * nb;
+    if (s.splits > 1 && part_bytes(B, a.Hq, s.splits, D) > workspace_bytes) return hipErrorInvalidValue;
     a.splits = s.splits;
     a.chunk = s.chunk;
     a.part = static_cast<float *>(workspace);

@@ -295,6 +295,55 @@ def test_layout_uses_every_byte_once(fmt, dim):
         assert sorted(taken) == list(range(0, size, step))
 
 
+SPLIT = r"""
+#include <cstdio>
+#include "attn_decode.hip"
+namespace qmm {
+hipError_t launch_attn_f16(int, int, const AttnArgs &, int64_t, hipStream_t) { return hipSuccess; }
+hipError_t launch_attn_q8_0(int, int, const AttnArgs &, int64_t, hipStream_t) { return hipSuccess; }
+hipError_t launch_attn_q4_0(int, int, const AttnArgs &, int64_t, hipStream_t) { return hipSuccess; }
+}
+using namespace qmm;
+int main() {
+    long long cases = 0, bad = 0;
+    const long long heads[][2] = {{1, 1}, {8, 1}, {32, 8}, {32, 32}, {14, 2}, {20, 1}, {64, 2}, {128, 16}, {17, 1}};
+    const long long lens[] = {1, 2, 255, 256, 257, 300, 511, 512, 513, 700, 1000, 1025, 4096, 5000, 40000, 131072, 1000003,
+                              (1LL << 31) - 8193};
+    for (auto &h : heads)
+        for (long long B = 1; B <= 1100; B += B < 80 ? 1 : 37)
+            for (long long n : lens)
+                for (long long w : {0LL, 1LL, 100LL, 500LL, 3000LL, n - 1, n, n + 5}) {
+                    if (w < 0) continue;
+                    const AttnSplit s = attn_split(B, h[0], h[1], n, w);
+                    const long long span = attn_span(n, w);
+                    ++cases;
+                    // the chunks cover the span, none is empty for every sequence, none is cut inside a group,
+                    // positions stay below 2^31, and the partial sums fit the workspace
+                    bool ok = s.splits >= 1 && s.chunk % kGroup == 0 && (long long)s.chunk * s.splits >= span &&
+                              (long long)s.chunk * (s.splits - 1) < span && (long long)s.chunk > 0 &&
+                              n + 8192 <= (1LL << 31) - 1;
+                    for (long long D : {64LL, 256LL})
+                        ok = ok && part_bytes(B, h[0], s.splits, D) <= attn_workspace(B, h[0], h[1], D, n, w);
+                    if (!ok && bad++ < 5) printf("bad %lld %lld %lld %lld %lld\n", h[0], h[1], B, n, w);
+                }
+    printf("cases %lld bad %lld\n", cases, bad);
+}
+"""
+
+
+@pytest.mark.skipif(HIPCC is None, reason="hipcc not found")
+def test_split_of_the_work_fits_the_workspace(tmp_path):
+    src, exe = tmp_path / "split.hip", tmp_path / "split"
+    src.write_text(SPLIT)
+    cmd = [HIPCC, "--offload-arch=gfx950", "-O1", "-std=c++17", "-I",
+           os.path.join(ROOT, "matmul_quantize_q8_amd", "csrc"), str(src), "-o", str(exe),
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    out = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    text = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60).stdout
+    assert text.strip().endswith("bad 0") and text.startswith("cases "), text
+
+
 # ---------------------------------------------------------------------------
 # The binding's checks
 # ---------------------------------------------------------------------------
