@@ -1,6 +1,7 @@
 """One attention block of a quantized model, token after token, on qmm.
 
     python examples/attention_decode.py [--tokens 64] [--cache q8_0] [--weights q4_0]
+        [--prompt 100] [--dim 1024] [--heads 16] [--kv-heads 4]
 
 Weights stay quantized, activations are f32.  A step is four launches (five
 where the attention is split over the cache's length):
@@ -112,10 +113,13 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--prompt", type=int, default=100)
+    ap.add_argument("--dim", type=int, default=1024)
+    ap.add_argument("--heads", type=int, default=16)
+    ap.add_argument("--kv-heads", type=int, default=4)
     ap.add_argument("--cache", choices=qmm.KV_FORMATS, default="q8_0")
     ap.add_argument("--weights", choices=qmm.FUSED_FORMATS, default="q4_0")
     a = ap.parse_args()
-    block = AttentionBlock(weights=a.weights, cache=a.cache, max_len=a.prompt + a.tokens)
+    block = AttentionBlock(a.dim, a.heads, a.kv_heads, a.weights, a.cache, max_len=a.prompt + a.tokens)
     gen = torch.Generator(device="cuda").manual_seed(1)
     dim = block.x.numel()
     block.prompt(torch.randn(a.prompt, dim, generator=gen, device="cuda"))

@@ -301,7 +301,8 @@ qmm_status qmm_get_rows_q5_1(const void *w, const int32_t *ids, float *out, int6
  * so slices of a fused QKV product can be passed as they are.  Pointers to rows
  * and both strides are multiples of four elements (QMM_E_ALIGN otherwise);
  * strides are not negative.  Index arrays (positions, slots, pages, lens) and
- * f32 arrays need the alignment of their type.  T, B, Hq, H >= 1. */
+ * f32 arrays need the alignment of their type.  T, B, Hq, H >= 1; T < 2^24,
+ * B < 2^16, Hq <= 4096. */
 typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
 
 /* Which two values of a row are rotated together, of the first `rot`: value i
@@ -439,7 +440,7 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, voi
  *   s_t = z + mask[b][t],   z = scale * q.k_t, or softcap * tanh(scale * q.k_t / softcap),
  *   out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = ln sum_t exp(s_t).
  * Position t is seen when t < lens[b], t >= lens[b] - window (window > 0) and
- * mask[b][t] is not -inf; nothing that the cache holds elsewhere, NaN included,
+ * mask[b][t] is not -inf (below -2.3e38 mask values count as equal); nothing that the cache holds elsewhere, NaN included,
  * reaches a result.  With no position seen, out is 0 and lse is -inf.  A
  * sequence whose length is outside [0, max_len], or with a page number outside
  * [0, n_pages) under a position that lens and window leave, gives NaN (no read

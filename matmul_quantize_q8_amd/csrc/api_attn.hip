@@ -21,6 +21,7 @@ using namespace qmm;
 
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxPage = 4096;
+constexpr int64_t kMaxTokens = (int64_t(1) << 24) - 1;   // a workgroup of 256 each: a grid holds 2^32 threads
 
 bool dtype_ok(int dt) { return dt == QMM_F32 || dt == QMM_F16 || dt == QMM_BF16; }
 
@@ -82,7 +83,7 @@ qmm_status check_index(const void *p, uintptr_t size) {
 qmm_status kv_write(int fmt, const qmm_rope_plan *plan, const qmm_kv_cache *cache, const void *q, void *q_out,
                     const void *k, const void *v, int dtype, const int32_t *positions, const int64_t *slots,
                     int64_t T, int64_t Hq, Strides qs, Strides qos, Strides ks, Strides vs, void *stream) {
-    if (!dtype_ok(dtype) || T < 1 || T > kMaxDim) return QMM_E_SHAPE;
+    if (!dtype_ok(dtype) || T < 1 || T > kMaxTokens) return QMM_E_SHAPE;
     WriteArgs a = {};
     QMM_TRY(check_cache(fmt, cache, a.c));
     const int64_t H = cache->heads, D = cache->dim;
@@ -114,7 +115,7 @@ qmm_status kv_write(int fmt, const qmm_rope_plan *plan, const qmm_kv_cache *cach
 
 qmm_status kv_read(int fmt, const qmm_kv_cache *cache, const int64_t *slots, void *k, void *v, int dtype, int64_t T,
                    Strides ks, Strides vs, void *stream) {
-    if (!dtype_ok(dtype) || T < 1 || T > kMaxDim) return QMM_E_SHAPE;
+    if (!dtype_ok(dtype) || T < 1 || T > kMaxTokens) return QMM_E_SHAPE;
     ReadArgs a = {};
     QMM_TRY(check_cache(fmt, cache, a.c));
     if (k == nullptr && v == nullptr) return QMM_E_NULL;
@@ -229,7 +230,7 @@ qmm_status qmm_rope_freqs(double *freqs, float *mscale, int64_t rot, double base
 qmm_status qmm_rope(const qmm_rope_plan *plan, const void *x, void *y, int dtype, const int32_t *positions,
                     int inverse, int64_t T, int64_t H, int64_t D, int64_t x_token_stride, int64_t x_head_stride,
                     int64_t y_token_stride, int64_t y_head_stride, void *stream) {
-    if (!dtype_ok(dtype) || T < 1 || T > kMaxDim || H < 1 || H > kMaxHeads) return QMM_E_SHAPE;
+    if (!dtype_ok(dtype) || T < 1 || T > kMaxTokens || H < 1 || H > kMaxHeads) return QMM_E_SHAPE;
     if (D < 4 || D > kMaxHeadDim || D % 4 != 0) return QMM_E_SHAPE;
     Rope r;
     QMM_TRY(check_plan(plan, D, inverse != 0, r));

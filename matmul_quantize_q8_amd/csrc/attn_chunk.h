@@ -419,8 +419,8 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
             const auto extra = [&](int t) {           // what the mask adds; -inf: not seen
                 if (t < lo || t >= to) return -INFINITY;
                 if (!a.mask) return 0.0f;
-                const float x = a.mask[b * a.mask_stride + t];
-                return x == -INFINITY ? x : fmaxf(x * kLog2e, -FLT_MAX);
+                const float x = a.mask[b * a.mask_stride + t], y = x * kLog2e;
+                return x == -INFINITY ? x : y < -FLT_MAX ? -FLT_MAX : y;    // the lowest f32 stays finite, NaN stays NaN
             };
 #pragma unroll
             for (int k = 0; k < 4 * NS; ++k) {

@@ -205,15 +205,21 @@ __device__ __forceinline__ float4 rotate4(const void *base, int64_t row, int n, 
 // A permlane swap exchanges the odd rows of 16 (or the upper 32 lanes) of one
 // register with the even rows (the lower 32) of the other: of two copies of x,
 // one comes back with the even row's value in both rows and the other with the
-// odd row's.  Written as instructions, with the wait that a register just
-// written needs, because the compiler's builtin yields its first result twice.
+// odd row's.  (The results are taken into scalars before the casts: a bit cast
+// of a vector's element yields element 0.)
 template <bool W32>
 __device__ __forceinline__ void swap_rows(float x, float &even, float &odd) {
-    even = odd = x;
-    if constexpr (W32)
-        asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
-    else
-        asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(even), "+v"(odd));
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    uint32_t a, b;
+    if constexpr (W32) {
+        const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        a = s[0], b = s[1];
+    } else {
+        const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        a = s[0], b = s[1];
+    }
+    even = __builtin_bit_cast(float, a);
+    odd = __builtin_bit_cast(float, b);
 }
 __device__ __forceinline__ float max_rows(float x) {
     float a, b;

@@ -52,7 +52,7 @@ def rope(L, plan=GOOD_PLAN, x=A, y=A + 4096, dt=0, pos=A, T=3, H=2, D=64, xs=(12
     (dict(plan=dict(GOOD_PLAN, rot=0)), 1), (dict(plan=dict(GOOD_PLAN, rot=63)), 1),
     (dict(plan=dict(GOOD_PLAN, rot=66)), 1), (dict(plan=dict(GOOD_PLAN, order=2)), 1),
     (dict(x=None), 2), (dict(y=None), 2), (dict(pos=None), 2), (dict(pos=A + 2), 3), (dict(x=A + 8), 3),
-    (dict(x=A + 4, dt=1), 3), (dict(dt=3), 1), (dict(dt=-1), 1), (dict(T=0), 1), (dict(T=1 << 31), 1),
+    (dict(x=A + 4, dt=1), 3), (dict(dt=3), 1), (dict(dt=-1), 1), (dict(T=0), 1), (dict(T=1 << 31), 1), (dict(T=1 << 24), 1),
     (dict(H=0), 1), (dict(H=4097), 1), (dict(D=66), 1), (dict(D=260), 1), (dict(xs=(126, 64)), 3),
     (dict(ys=(128, 62)), 3), (dict(xs=(-128, 64)), 1), (dict(xs=(1 << 39, 64)), 1), (dict(xs=(1 << 62, 1 << 62)), 1),
 ])

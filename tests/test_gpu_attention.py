@@ -409,6 +409,24 @@ def test_attention_mask(env, fmt, extra):
     s.check(mask=mask)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_mask_nan(env, fmt):
+    """NaN in a mask reaches the rows that see its position and no others; past the
+    length, and before the window, the mask is not looked at."""
+    torch, q, _ = env
+    _say("attention mask nan", fmt)
+    s = Setup(env, fmt, [100, 100, 100, 70], 4, 2, 64, 16, "f32", 6)
+    mask = np.zeros((4, 100), np.float32)
+    mask[0, 99] = mask[1, 40] = np.nan
+    mask[3, 70:] = np.nan
+    s.run(mask=_dev(torch, mask))
+    assert np.isnan(_np(s.out)[:2]).all() and np.isnan(_np(s.lse)[:2]).all()
+    s.check(mask=np.nan_to_num(mask), rows=[2, 3])
+    s.run(mask=_dev(torch, mask), window=50)
+    assert np.isnan(_np(s.out)[0]).all()
+    s.check(mask=np.nan_to_num(mask), rows=[1, 2, 3], window=50)
+
+
 def test_attention_infinities(env):
     """Inf and NaN in rows that are seen make the result's columns (a key's: the
     whole row) infinite or NaN, and no others."""
