@@ -309,6 +309,7 @@ QUANTIZE_MATVEC = {"q4_0": qmm_quantize_matvec_q4_0, "q8_0": qmm_quantize_matvec
 GET_ROWS = {f: globals()["qmm_get_rows_" + f] for f in WEIGHT_FORMATS}
 
 # -- attention ------------------------------------------------------------------
+_attention.bind(_call, _stream, lib)
 KV_FORMATS = _attention.KV_FORMATS
 RopePlan, KVCache = _attention.RopePlan, _attention.KVCache
 kv_page_bytes, attn_workspace = _attention.kv_page_bytes, _attention.attn_workspace

@@ -53,29 +53,33 @@ def declare(L) -> None:
     L.qmm_attn_decode_workspace.restype = I64
 
 
-def _qmm():
-    import matmul_quantize_q8_amd as q
-    return q
+# Set by the package: its call, stream and library access.
+_call = _stream = _lib = None
 
 
-_types = None
+def bind(call, stream, lib) -> None:
+    global _call, _stream, _lib
+    _call, _stream, _lib = call, stream, lib
 
 
-def _dtype(t) -> int:
-    global _types
-    if _types is None:
+# torch, imported at the first use of it, and the row types' codes.
+_torch = None
+_CODES = {}
+
+
+def _t():
+    global _torch
+    if _torch is None:
         import torch
-        _types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    try:
-        return _types[t.dtype]
-    except KeyError:
-        raise ValueError(f"rows are float32, float16 or bfloat16, not {t.dtype}") from None
+        _CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        _torch = torch
+    return _torch
 
 
 def _rows(name, t, shape, dtype):
     """(address, token stride, head stride) of rows of that shape and type."""
     if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name}: want {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     token, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the values of a row have to be contiguous")
@@ -84,11 +88,26 @@ def _rows(name, t, shape, dtype):
     return t.data_ptr(), token, head
 
 
+def _code(dtype) -> int:
+    c = _CODES.get(dtype)
+    if c is None:
+        raise ValueError(f"rows are float32, float16 or bfloat16, not {dtype}")
+    return c
+
+
+def _three(name, t):
+    """The shape of rows."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: want rows [tokens][heads][dim], got {tuple(shape)}")
+    return shape
+
+
 def _array(name, t, dtype, shape):
     """Address of a contiguous array on the GPU."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: want a contiguous {dtype} {shape} on the GPU, got {t.dtype} {tuple(t.shape)}"
-                         f" on {t.device}")
+        raise ValueError(f"{name}: want a contiguous {dtype} {tuple(shape)} on the GPU, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -96,13 +115,12 @@ def _array(name, t, dtype, shape):
 def qmm_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
                    trained_len: float = 0.0, low: float = 0.0, high: float = 0.0):
     """(frequencies, mscale) of a rotation of `rot` values: a float64 CPU tensor [rot/2] and a float."""
-    import torch
-    q = _qmm()
+    torch = _t()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling is one of {', '.join(ROPE_SCALINGS)}, not {scaling!r}")
     out, ms = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64), ctypes.c_float()
-    q._call("qmm_rope_freqs", out.data_ptr(), ctypes.addressof(ms), rot, base, ROPE_SCALINGS[scaling], factor,
-            trained_len, low, high)
+    _call("qmm_rope_freqs", out.data_ptr(), ctypes.addressof(ms), rot, base, ROPE_SCALINGS[scaling], factor,
+          trained_len, low, high)
     return out, ms.value
 
 
@@ -111,7 +129,7 @@ class RopePlan:
     the pairs ("half" or "interleaved") and the factor on cosine and sine."""
 
     def __init__(self, freqs, order: str = "half", mscale: float = 1.0):
-        import torch
+        torch = _t()
         if order not in ROPE_ORDERS:
             raise ValueError(f"order is one of {', '.join(ROPE_ORDERS)}, not {order!r}")
         self.freqs = freqs
@@ -124,21 +142,17 @@ def qmm_rope(x, y, positions, plan: RopePlan, inverse: bool = False, stream=None
     """y = x [T][H][D] with the first rot values of every row rotated to its
     token's position (int32 [T]); inverse: by the negative angle, which takes
     the gradient of y to that of x.  y may be x."""
-    import torch
-    q = _qmm()
-    shape = tuple(x.shape)
-    if len(shape) != 3:
-        raise ValueError(f"x: want rows [tokens][heads][dim], got {shape}")
-    xa, xt, xh = _rows("x", x, shape, x.dtype)
-    ya, yt, yh = _rows("y", y, shape, x.dtype)
-    q._call("qmm_rope", plan._p, xa, ya, _dtype(x), _array("positions", positions, torch.int32, shape[:1]),
-            int(inverse), *shape, xt, xh, yt, yh, q._stream(stream))
+    torch, shape, dtype = _t(), _three("x", x), x.dtype
+    xa, xt, xh = _rows("x", x, shape, dtype)
+    ya, yt, yh = _rows("y", y, shape, dtype)
+    _call("qmm_rope", plan._p, xa, ya, _code(dtype), _array("positions", positions, torch.int32, shape[:1]),
+          1 if inverse else 0, shape[0], shape[1], shape[2], xt, xh, yt, yh, _stream(stream))
 
 
 # -- cache ----------------------------------------------------------------------
 def kv_page_bytes(fmt: str, page: int, heads: int, dim: int) -> int:
     """Bytes of one page of a cache in `fmt` (0 for sizes outside the limits)."""
-    return getattr(_qmm().lib(), "qmm_kv_page_bytes_" + fmt)(page, heads, dim)
+    return getattr(_lib(), "qmm_kv_page_bytes_" + fmt)(page, heads, dim)
 
 
 def _page_bytes(fmt):
@@ -154,7 +168,7 @@ class KVCache:
     on the GPU of a whole number of pages (KVCache.empty makes one)."""
 
     def __init__(self, fmt: str, data, page: int, heads: int, dim: int):
-        import torch
+        torch = _t()
         if fmt not in KV_FORMATS:
             raise ValueError(f"the cache's format is one of {', '.join(KV_FORMATS)}, not {fmt!r}")
         size = kv_page_bytes(fmt, page, heads, dim)
@@ -171,8 +185,7 @@ class KVCache:
     @classmethod
     def empty(cls, fmt: str, n_pages: int, page: int, heads: int, dim: int, device="cuda"):
         """A new cache; its rows hold nothing until they are written."""
-        import torch
-        return cls(fmt, torch.empty(n_pages * kv_page_bytes(fmt, page, heads, dim), dtype=torch.uint8, device=device),
+        return cls(fmt, _t().empty(n_pages * kv_page_bytes(fmt, page, heads, dim), dtype=_torch.uint8, device=device),
                    page, heads, dim)
 
 
@@ -186,13 +199,12 @@ def _kv_write(fmt):
     name = "qmm_kv_write_" + fmt
 
     def kv_write(k, v, cache: KVCache, slots, stream=None) -> None:
-        import torch
-        q = _qmm()
-        shape = (k.shape[0], cache.heads, cache.dim)
-        ka, kt, kh = _rows("k", k, shape, k.dtype)
-        va, vt, vh = _rows("v", v, shape, k.dtype)
-        q._call(name, _of(cache, fmt), ka, va, _dtype(k), _array("slots", slots, torch.int64, shape[:1]), shape[0],
-                kt, kh, vt, vh, q._stream(stream))
+        torch, dtype, T = _t(), k.dtype, k.shape[0]
+        shape = (T, cache.heads, cache.dim)
+        ka, kt, kh = _rows("k", k, shape, dtype)
+        va, vt, vh = _rows("v", v, shape, dtype)
+        _call(name, _of(cache, fmt), ka, va, _code(dtype), _array("slots", slots, torch.int64, (T,)), T, kt, kh, vt,
+              vh, _stream(stream))
     kv_write.__name__ = name
     kv_write.__doc__ = f"Write keys and values [T][H][D] into the slots (int64 [T]) of a {fmt} cache."
     return kv_write
@@ -202,20 +214,15 @@ def _rope_kv_write(fmt):
     name = "qmm_rope_kv_write_" + fmt
 
     def rope_kv_write(q, q_out, k, v, cache: KVCache, slots, positions, plan: RopePlan, stream=None) -> None:
-        import torch
-        m = _qmm()
-        shape = (k.shape[0], cache.heads, cache.dim)
-        if q.dim() != 3:
-            raise ValueError(f"q: want rows [tokens][heads][dim], got {tuple(q.shape)}")
-        qshape = (shape[0], q.shape[1], cache.dim)
-        qa, qt, qh = _rows("q", q, qshape, k.dtype)
-        oa, ot, oh = _rows("q_out", q_out, qshape, k.dtype)
-        ka, kt, kh = _rows("k", k, shape, k.dtype)
-        va, vt, vh = _rows("v", v, shape, k.dtype)
-        m._call(name, plan._p, _of(cache, fmt), qa, oa, ka, va, _dtype(k),
-                _array("positions", positions, torch.int32, shape[:1]),
-                _array("slots", slots, torch.int64, shape[:1]), shape[0], qshape[1], qt, qh, ot, oh, kt, kh, vt, vh,
-                m._stream(stream))
+        torch, dtype, T = _t(), k.dtype, k.shape[0]
+        shape, qshape = (T, cache.heads, cache.dim), (T, _three("q", q)[1], cache.dim)
+        qa, qt, qh = _rows("q", q, qshape, dtype)
+        oa, ot, oh = _rows("q_out", q_out, qshape, dtype)
+        ka, kt, kh = _rows("k", k, shape, dtype)
+        va, vt, vh = _rows("v", v, shape, dtype)
+        _call(name, plan._p, _of(cache, fmt), qa, oa, ka, va, _code(dtype),
+              _array("positions", positions, torch.int32, (T,)), _array("slots", slots, torch.int64, (T,)), T,
+              qshape[1], qt, qh, ot, oh, kt, kh, vt, vh, _stream(stream))
     rope_kv_write.__name__ = name
     rope_kv_write.__doc__ = (f"Rotate queries into q_out and write the rotated keys and the values into the slots "
                              f"of a {fmt} cache, in one launch.")
@@ -226,16 +233,16 @@ def _kv_read(fmt):
     name = "qmm_kv_read_" + fmt
 
     def kv_read(cache: KVCache, slots, k, v, stream=None) -> None:
-        import torch
-        q = _qmm()
+        torch = _t()
         some = k if k is not None else v
         if some is None:
             raise ValueError("neither k nor v is wanted")
-        shape = (slots.shape[0], cache.heads, cache.dim)
-        ka, kt, kh = _rows("k", k, shape, some.dtype) if k is not None else (None, 0, 0)
-        va, vt, vh = _rows("v", v, shape, some.dtype) if v is not None else (None, 0, 0)
-        q._call(name, _of(cache, fmt), _array("slots", slots, torch.int64, shape[:1]), ka, va, _dtype(some), shape[0],
-                kt, kh, vt, vh, q._stream(stream))
+        dtype, T = some.dtype, slots.shape[0]
+        shape = (T, cache.heads, cache.dim)
+        ka, kt, kh = _rows("k", k, shape, dtype) if k is not None else (None, 0, 0)
+        va, vt, vh = _rows("v", v, shape, dtype) if v is not None else (None, 0, 0)
+        _call(name, _of(cache, fmt), _array("slots", slots, torch.int64, (T,)), ka, va, _code(dtype), T, kt, kh, vt,
+              vh, _stream(stream))
     kv_read.__name__ = name
     kv_read.__doc__ = (f"Read the slots (int64 [T]) of a {fmt} cache back into k and v [T][H][D] (either may be None; "
                        "NaN rows for slots outside the cache).")
@@ -245,16 +252,15 @@ def _kv_read(fmt):
 # -- attention ------------------------------------------------------------------
 def qmm_attn_decode_workspace(B: int, Hq: int, heads: int, dim: int, max_len: int, window: int = 0) -> int:
     """Bytes of the workspace of qmm_attn_decode_* (0 for sizes outside the limits)."""
-    return _qmm().lib().qmm_attn_decode_workspace(B, Hq, heads, dim, max_len, window)
+    return _lib().qmm_attn_decode_workspace(B, Hq, heads, dim, max_len, window)
 
 
 def attn_workspace(B: int, Hq: int, heads: int, dim: int, max_len: int, window: int = 0, device="cuda"):
     """A new workspace for qmm_attn_decode_*, enough for smaller batches and lengths too."""
-    import torch
     size = qmm_attn_decode_workspace(B, Hq, heads, dim, max_len, window)
     if size == 0:
         raise ValueError(f"no attention of batch {B}, {Hq} on {heads} heads of {dim}, length {max_len}")
-    return torch.empty(size, dtype=torch.uint8, device=device)
+    return _t().empty(size, dtype=_torch.uint8, device=device)
 
 
 def _attn_decode(fmt):
@@ -262,24 +268,22 @@ def _attn_decode(fmt):
 
     def attn_decode(q, out, cache: KVCache, pages, lens, max_len: int, workspace, scale=None, softcap: float = 0.0,
                     window: int = 0, mask=None, lse=None, stream=None) -> None:
-        import torch
-        m = _qmm()
-        if q.dim() != 3:
-            raise ValueError(f"q: want rows [sequences][heads][dim], got {tuple(q.shape)}")
-        shape = (q.shape[0], q.shape[1], cache.dim)
-        B = shape[0]
-        qa, qt, qh = _rows("q", q, shape, q.dtype)
-        oa, ot, oh = _rows("out", out, shape, q.dtype)
+        torch, dtype = _t(), q.dtype
+        B, Hq, _ = _three("q", q)
+        shape = (B, Hq, cache.dim)
+        qa, qt, qh = _rows("q", q, shape, dtype)
+        oa, ot, oh = _rows("out", out, shape, dtype)
+        width = pages.shape[-1]
         ma, ms = None, 0
         if mask is not None:
             ms = mask.shape[-1]
             ma = _array("mask", mask, torch.float32, (B, ms))
-        m._call(name, _of(cache, fmt), qa, oa, _dtype(q), _array("pages", pages, torch.int32, (B, pages.shape[-1])),
-                pages.shape[-1], _array("lens", lens, torch.int32, (B,)), B, shape[1], max_len,
-                1.0 / math.sqrt(cache.dim) if scale is None else scale, softcap, window, ma, ms,
-                None if lse is None else _array("lse", lse, torch.float32, shape[:2]), qt, qh, ot, oh,
-                _array("workspace", workspace, torch.uint8, (workspace.numel(),)), workspace.numel(),
-                m._stream(stream))
+        size = workspace.numel()
+        _call(name, _of(cache, fmt), qa, oa, _code(dtype), _array("pages", pages, torch.int32, (B, width)), width,
+              _array("lens", lens, torch.int32, (B,)), B, Hq, max_len,
+              1.0 / math.sqrt(cache.dim) if scale is None else scale, softcap, window, ma, ms,
+              None if lse is None else _array("lse", lse, torch.float32, (B, Hq)), qt, qh, ot, oh,
+              _array("workspace", workspace, torch.uint8, (size,)), size, _stream(stream))
     attn_decode.__name__ = name
     attn_decode.__doc__ = (
         f"Attention of one new token of each sequence over a {fmt} cache: q, out [B][Hq][D]; pages int32 "
