@@ -22,10 +22,14 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(Rope r, const void *x, vo
     const int quads = D >> 2, per_wave = 64 / quads, sub = lane / quads, n = 4 * (lane - sub * quads);
     if (sub >= per_wave) return;
     const int step = gridDim.y * (kRopeThreads / 64) * per_wave;
-    for (int h = (blockIdx.y * (kRopeThreads / 64) + wave) * per_wave + sub; h < H; h += step) {
+    int h = (blockIdx.y * (kRopeThreads / 64) + wave) * per_wave + sub;
+    for (; h + step < H; h += 2 * step) {                 // two rows' loads in flight: neither store may pass them
         const float4 v = rotate4<RT>(x, t * xs.token + h * xs.head, n, r, cs);
+        const float4 w = rotate4<RT>(x, t * xs.token + (h + step) * xs.head, n, r, cs);
         store4<RT>(y, t * ys.token + h * ys.head + n, v);
+        store4<RT>(y, t * ys.token + (h + step) * ys.head + n, w);
     }
+    if (h < H) store4<RT>(y, t * ys.token + h * ys.head + n, rotate4<RT>(x, t * xs.token + h * xs.head, n, r, cs));
 }
 
 // Parts of a token's rows: as many workgroups as give the chip four a compute
