@@ -1,13 +1,17 @@
 // The paged key-value cache: rows quantized as they are written (with the
 // rotation of queries and keys in the same launch), and read back.
 //
-// Reading, a workgroup takes 16 tokens; a wave takes the rows of one head of all 16, in
-// the lanes of the cache's byte order: for keys (and queries) lane (g, r) holds
-// of token r the values 32b + 8g + i, for values lane (g, m) holds of tokens
-// 4g + i the values 32b + 2m + e.  So 16 tokens of one aligned group, which is
-// what a prompt writes and reads, move as whole lines of the cache and as 64-byte
-// pieces of the rows; tokens with slots anywhere take the same path, each lane
-// with its own address.
+// Writing, a workgroup takes one token and its waves whole rows, 16 bytes a lane:
+// 4096 tokens of 32 + 8 + 8 heads of 128 in bf16 (93 MB) take 22 us, 4.2 TB/s of
+// the 4.9 of a large copy.  Reading, a workgroup takes 16 tokens; a wave takes the
+// rows of one head of all 16, in the lanes of the cache's byte order: for keys lane
+// (g, r) holds of token r the values 32b + 8g + i, for values lane (g, m) holds of
+// tokens 4g + i the values 32b + 2m + e.  So 16 tokens of one aligned group, which
+// is what a prompt reads, move as whole lines of the cache and as 64-byte pieces of
+// the rows; tokens with slots anywhere take the same path, each lane with its own
+// address.  8192 tokens q8_0 to bf16 (51 MB): 22 us a token a workgroup, 12 us so.
+// (Writing in that order took 41 us: a token's table of angles for each of 16
+// tokens, and half the waves.)
 //
 // Bit-exactness: as in quantize.hip, every step of a quantizer is one correctly
 // rounded f32 operation, so a row's codes and scales are those of the weight
@@ -44,76 +48,88 @@ __device__ __forceinline__ void load_row_scales(const uint8_t *p, float (&d)[NB]
 // ---------------------------------------------------------------------------
 // Writing
 // ---------------------------------------------------------------------------
-// Codes of a block's quad (four of 32 values, eight lanes a block), one a byte
-// and offset to be unsigned; d is the block's scale.  All eight lanes call it.
-template <int F>
-__device__ __forceinline__ uint32_t quad_codes(float4 v, int part, float &d) {
+// Codes of V consecutive values of a block, in 32 / V lanes, offset to be
+// unsigned, and the block's scale.  All lanes of the block call it.
+template <int F, int V>
+__device__ __forceinline__ void block_codes(const float (&v)[V], int part, uint32_t (&c)[V], float &d) {
+    float a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a = fmaxf(a, fabsf(v[k]));
+    a = fmaxf(a, dpp_f32<kDppQuadXor1>(a));
+    a = fmaxf(a, dpp_f32<kDppQuadXor2>(a));
+    if constexpr (V == 4) a = fmaxf(a, dpp_f32<kDppHalfRowMirror>(a));
     if constexpr (F == KV_Q8_0) {
-        return q8_0_part(v, d) ^ 0x80808080u;
+        d = a / 127.0f;
+        const float id = a != 0.0f ? 127.0f / a : 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) c[k] = (uint32_t)((int)rintf(v[k] * id) + 128) & 255u;
     } else {
-        const float vv[4] = {v.x, v.y, v.z, v.w};
-        float am = fabsf(vv[0]), mx = vv[0];              // largest magnitude, the first on ties
-        int ix = 4 * part;
+        // the sign of the value of largest magnitude, the first on ties: the least
+        // 2 * number + sign among the values of that magnitude
+        float key = 1000.0f;
 #pragma unroll
-        for (int k = 1; k < 4; ++k) {
-            const float a = fabsf(vv[k]);
-            if (a > am) { am = a; mx = vv[k]; ix = 4 * part + k; }
-        }
+        for (int k = V - 1; k >= 0; --k)
+            if (fabsf(v[k]) == a) key = (float)(2 * (V * part + k) + (v[k] < 0.0f));
+        key = fminf(key, dpp_f32<kDppQuadXor1>(key));
+        key = fminf(key, dpp_f32<kDppQuadXor2>(key));
+        if constexpr (V == 4) key = fminf(key, dpp_f32<kDppHalfRowMirror>(key));
+        const float mx = ((int)key & 1) ? -a : a;
+        d = a != 0.0f ? mx / -8.0f : 0.0f;
 #pragma unroll
-        for (int m = 1; m < 8; m <<= 1) {
-            const float oam = xor_shfl(am, m), omx = xor_shfl(mx, m);
-            const int oix = xor_shfl(ix, m);
-            if (oam > am || (oam == am && oix < ix)) { am = oam; mx = omx; ix = oix; }
+        for (int k = 0; k < V; ++k) {
+            const int q = d != 0.0f ? (int)rintf(v[k] / d) + 8 : 8;
+            c[k] = (uint32_t)min(max(q, 0), 15);
         }
-        d = am != 0.0f ? mx / -8.0f : 0.0f;
-        uint32_t codes = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            int c = d != 0.0f ? (int)rintf(vv[k] / d) + 8 : 8;
-            codes |= (uint32_t)min(max(c, 0), 15) << (8 * k);
-        }
-        return codes;
     }
 }
 
-// Store a quad at `side` (one head's keys or values of one page).
-template <int F, int NB>
-__device__ __forceinline__ void store_quad(uint8_t *side, int page, int t, int quad, bool values, float4 v) {
+// The low BYTES bytes of w at p, aligned to them.
+template <int BYTES>
+__device__ __forceinline__ void store_piece(uint8_t *p, const uint32_t *w) {
+    if constexpr (BYTES == 1)
+        *p = (uint8_t)*w;
+    else if constexpr (BYTES == 2)
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)*w;
+    else {
+        Unit<BYTES> u;
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) u.w[i] = w[i];
+        *reinterpret_cast<Unit<BYTES> *>(p) = u;
+    }
+}
+
+// Store values V part .. of a row of position t at `side` (one head's keys or
+// values of one page).  A key's V are consecutive in their lane's bytes; a
+// value's are two in each of V/2 lanes.
+template <int F, int NB, int V>
+__device__ __forceinline__ void store_values(uint8_t *side, int page, int t, int lane, bool values,
+                                             const float (&v)[V]) {
     using K = Kv<F, NB>;
-    const int b = quad >> 3, part = quad & 7, e = K::byte_of(b * 8 + (part & 1) * 4), w = K::byte_of(2 * b);
-    uint8_t *const kp = side + K::key_unit(t, part >> 1, e / K::U) + e % K::U;
-    uint8_t *const v0 = side + K::value_byte(t, 2 * part, w), *const v1 = side + K::value_byte(t, 2 * part + 1, w);
+    constexpr int kBits = kv_bits(F), kBlockLanes = 32 / V;
+    const int b = lane / kBlockLanes, part = lane % kBlockLanes, first = V * part;
+    uint32_t c[V];
     if constexpr (F == KV_F16) {
-        const uint32_t lo = pack2<R_F16>(v.x, v.y), hi = pack2<R_F16>(v.z, v.w);
-        if (values) {
-            *reinterpret_cast<uint32_t *>(v0) = lo;
-            *reinterpret_cast<uint32_t *>(v1) = hi;
-        } else {
-            *reinterpret_cast<uint2 *>(kp) = make_uint2(lo, hi);
-        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) c[k] = f32_to_f16_bits(v[k]);
     } else {
         float d;
-        const uint32_t c = quad_codes<F>(v, part, d);
-        if constexpr (F == KV_Q8_0) {
-            if (values) {
-                *reinterpret_cast<uint16_t *>(v0) = (uint16_t)c;
-                *reinterpret_cast<uint16_t *>(v1) = (uint16_t)(c >> 16);
-            } else {
-                *reinterpret_cast<uint32_t *>(kp) = c;
-            }
-        } else {
-            const uint32_t two = c | (c >> 4);            // bytes 0 and 2: the pairs' nibbles
-            if (values) {
-                *v0 = (uint8_t)two;
-                *v1 = (uint8_t)(two >> 16);
-            } else {
-                *reinterpret_cast<uint16_t *>(kp) =
-                    (uint16_t)((two & 0xffu) | ((two >> 8) & 0xff00u));
-            }
-        }
-        if (part == 0) {
+        block_codes<F, V>(v, part, c, d);
+        if (part == 0)
             *reinterpret_cast<uint16_t *>(side + K::scale_byte(page, t) + 2 * b) = (uint16_t)f32_to_f16_bits(d);
+    }
+    uint32_t w[(V * kBits + 31) / 32] = {};
+#pragma unroll
+    for (int k = 0; k < V; ++k) w[k * kBits / 32] |= c[k] << (k * kBits % 32);
+    if (values) {
+        const int byte = K::byte_of(2 * b);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const uint32_t two = w[k * kBits / 32] >> (k * kBits % 32);
+            store_piece<kBits / 4>(side + K::value_byte(t, (first + k) / 2, byte), &two);
         }
+    } else {
+        const int byte = K::byte_of(b * 8 + first % 8);
+        store_piece<V * kBits / 8>(side + K::key_unit(t, first / 8, byte / K::U) + byte % K::U, w);
     }
 }
 
@@ -128,10 +144,10 @@ __device__ __forceinline__ int64_t token_of(int64_t i, int64_t T) {
 }
 
 // One workgroup a token (and part of its rows): query rows, then key rows, then
-// value rows, each by D/4 lanes of one wave.
+// value rows, each by D/V lanes of one wave.
 template <int F, int NB, int RT>
 __global__ __launch_bounds__(kRowThreads) void k_kv_write(WriteArgs a) {
-    constexpr int kQuads = 8 * NB, kPer = 64 / kQuads;
+    constexpr int V = row_values(RT), kLanes = 32 * NB / V, kPer = 64 / kLanes;
     __shared__ float2 cs[kMaxHeadDim / 2];
     const int64_t t = token_of(blockIdx.x, a.T);
     if (a.r.rot) {
@@ -139,7 +155,7 @@ __global__ __launch_bounds__(kRowThreads) void k_kv_write(WriteArgs a) {
         __syncthreads();
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int sub = lane / kQuads, quad = lane - sub * kQuads;
+    const int sub = lane / kLanes, at_lane = lane - sub * kLanes, n = V * at_lane;
     if (sub >= kPer) return;
     const int page = 1 << a.c.page_shift;
     const int64_t slot = a.slots[t], pg = slot >> a.c.page_shift;
@@ -147,17 +163,20 @@ __global__ __launch_bounds__(kRowThreads) void k_kv_write(WriteArgs a) {
     const int at = (int)(slot & (page - 1));
     const int64_t side = Kv<F, NB>::side_bytes(page);
     uint8_t *base = a.c.page_at(keep ? pg : 0, side);
-    const int H = a.c.heads, rows = a.Hq + 2 * H, step = gridDim.y * (kRowThreads / 64) * kPer;
-    for (int row = (blockIdx.y * (kRowThreads / 64) + wave) * kPer + sub; row < rows; row += step) {
+    const int H = a.c.heads, rows = a.Hq + 2 * H, step = gridDim.y * kRowWaves * kPer;
+    for (int row = (blockIdx.y * kRowWaves + wave) * kPer + sub; row < rows; row += step) {
+        float y[V];
         if (row < a.Hq) {
-            const float4 y = rotate4<RT>(a.q, t * a.qs.token + row * a.qs.head, 4 * quad, a.r, cs);
-            store4<RT>(a.qo, t * a.qos.token + row * a.qos.head + 4 * quad, y);
+            rotate<RT, V>(a.q, t * a.qs.token + row * a.qs.head, n, a.r, cs, y);
+            store_row<RT, V>(a.qo, t * a.qos.token + row * a.qos.head + n, y);
         } else {
             const bool values = row >= a.Hq + H;
             const int h = row - a.Hq - (values ? H : 0);
-            const float4 y = values ? load4<RT>(a.v, t * a.vs.token + h * a.vs.head + 4 * quad)
-                                    : rotate4<RT>(a.k, t * a.ks.token + h * a.ks.head, 4 * quad, a.r, cs);
-            if (keep) store_quad<F, NB>(base + (2 * h + values) * side, page, at, quad, values, y);
+            if (values)
+                load_row<RT, V>(a.v, t * a.vs.token + h * a.vs.head + n, y);
+            else
+                rotate<RT, V>(a.k, t * a.ks.token + h * a.ks.head, n, a.r, cs, y);
+            if (keep) store_values<F, NB, V>(base + (2 * h + values) * side, page, at, at_lane, values, y);
         }
     }
 }
@@ -250,7 +269,8 @@ __global__ __launch_bounds__(kRowThreads) void k_kv_read(ReadArgs a) {
 
 template <int F, int NB>
 static hipError_t launch_write_f(int rt, WriteArgs a, hipStream_t st) {
-    const dim3 grid((unsigned)a.T, (unsigned)row_parts(a.T, a.Hq + 2 * a.c.heads, kRowWaves * (64 / (8 * NB))));
+    const int per_wave = 64 / (32 * NB / row_values(rt));
+    const dim3 grid((unsigned)a.T, (unsigned)row_parts(a.T, a.Hq + 2 * a.c.heads, kRowWaves * per_wave));
     void *args[] = {(void *)&a};
     const void *k = rt == R_F32   ? (const void *)k_kv_write<F, NB, R_F32>
                     : rt == R_F16 ? (const void *)k_kv_write<F, NB, R_F16>

@@ -120,13 +120,50 @@ __device__ __forceinline__ void rope_table(const Rope &r, int32_t pos, float2 *c
     }
 }
 
-// Eight consecutive values; base and i as for load4.
-template <int RT>
-__device__ __forceinline__ void load8(const void *base, int64_t i, float (&x)[8]) {
-    const float4 a = load4<RT>(base, i), b = load4<RT>(base, i + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Values a lane takes of a row: 16 bytes.
+constexpr int row_values(int rt) { return rt == R_F32 ? 4 : 8; }
+
+// V consecutive values; base and i as for load4.
+template <int RT, int V>
+__device__ __forceinline__ void load_row(const void *base, int64_t i, float (&x)[V]) {
+    static_assert(V == 4 || (V == 8 && RT != R_F32), "");
+    if constexpr (V == 4) {
+        const float4 v = load4<RT>(base, i);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {                                              // one load, though only aligned to eight bytes
+        struct __attribute__((packed, aligned(8))) Words { uint32_t w[4]; };
+        const Words u = *reinterpret_cast<const Words *>(static_cast<const uint16_t *>(base) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = RT == R_F16 ? f16_bits_to_f32(u.w[k]) : __builtin_bit_cast(float, u.w[k] << 16);
+            x[2 * k + 1] = RT == R_F16 ? f16_bits_to_f32(u.w[k] >> 16)
+                                       : __builtin_bit_cast(float, u.w[k] & 0xffff0000u);
+        }
+    }
 }
+template <int RT, int V>
+__device__ __forceinline__ void store_row(void *base, int64_t i, const float (&x)[V]) {
+    if constexpr (V == 4) {
+        store4<RT>(base, i, make_float4(x[0], x[1], x[2], x[3]));
+    } else {
+        struct __attribute__((packed, aligned(8))) Words { uint32_t w[4]; } u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u.w[k] = pack2<RT>(x[2 * k], x[2 * k + 1]);
+        *reinterpret_cast<Words *>(static_cast<uint16_t *>(base) + i) = u;
+    }
+}
+
+// Eight values for the cache's reader.
+template <int RT>
+__device__ __forceinline__ void store8(void *base, int64_t i, const float (&x)[8]) {
+    if constexpr (RT == R_F32) {
+        store4<RT>(base, i, make_float4(x[0], x[1], x[2], x[3]));
+        store4<RT>(base, i + 4, make_float4(x[4], x[5], x[6], x[7]));
+    } else {
+        store_row<RT, 8>(base, i, x);
+    }
+}
+
 // Two consecutive values; i is even.
 template <int RT>
 __device__ __forceinline__ void load2(const void *base, int64_t i, float (&x)[2]) {
@@ -146,56 +183,46 @@ __device__ __forceinline__ void store2(void *base, int64_t i, const float (&x)[2
     else
         *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + i) = pack2<RT>(x[0], x[1]);
 }
-template <int RT>
-__device__ __forceinline__ void store8(void *base, int64_t i, const float (&x)[8]) {
-    store4<RT>(base, i, make_float4(x[0], x[1], x[2], x[3]));
-    store4<RT>(base, i + 4, make_float4(x[4], x[5], x[6], x[7]));
-}
-
-// Values n .. n+3 of the rotated row that starts at element `row` of `base`.
+// Values n .. n+V-1 of the rotated row that starts at element `row` of `base`.
 // The pair's other value is read from memory again: the row is in the cache.
-template <int RT>
-__device__ __forceinline__ float4 rotate4(const void *base, int64_t row, int n, const Rope &r, const float2 *cs) {
-    const float4 x4 = load4<RT>(base, row + n);
-    if (n >= r.rot) return x4;
-    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-    float y[4];
+template <int RT, int V>
+__device__ __forceinline__ void rotate(const void *base, int64_t row, int n, const Rope &r, const float2 *cs,
+                                       float (&y)[V]) {
+    load_row<RT, V>(base, row + n, y);
+    if (n >= r.rot) return;
+    const int half = r.rot >> 1;
     if (r.order) {                                        // interleaved: both values of a pair are here
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
+        for (int k = 0; k < V; k += 2) {
             const bool in = n + k < r.rot;
             const float2 t = cs[in ? (n + k) >> 1 : 0];
-            y[k] = in ? x[k] * t.x - x[k + 1] * t.y : x[k];
-            y[k + 1] = in ? x[k] * t.y + x[k + 1] * t.x : x[k + 1];
+            const float u = y[k], v = y[k + 1];
+            y[k] = in ? u * t.x - v * t.y : u;
+            y[k + 1] = in ? u * t.y + v * t.x : v;
+        }
+    } else if (half % V == 0) {                           // the V partners are aligned together
+        const bool first = n < half;
+        const int pair = first ? n : n - half;
+        float p[V];
+        load_row<RT, V>(base, row + (first ? n + half : pair), p);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float2 t = cs[pair + k];
+            y[k] = first ? y[k] * t.x - p[k] * t.y : p[k] * t.y + y[k] * t.x;
         }
     } else {
-        const int half = r.rot >> 1;
-        if ((half & 3) == 0) {                            // the four partners are aligned together
-            const bool first = n < half;
-            const int pair = first ? n : n - half;
-            const float4 p4 = load4<RT>(base, row + (first ? n + half : pair));
-            const float p[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 t = cs[pair + k];
-                y[k] = first ? x[k] * t.x - p[k] * t.y : p[k] * t.y + x[k] * t.x;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = n + k;
-                y[k] = x[k];
-                if (i < r.rot) {
-                    const bool first = i < half;
-                    const int pair = first ? i : i - half;
-                    const float2 t = cs[pair];
-                    const float p = load1<RT>(base, row + (first ? i + half : pair));
-                    y[k] = first ? x[k] * t.x - p * t.y : p * t.y + x[k] * t.x;
-                }
+        for (int k = 0; k < V; ++k) {
+            const int i = n + k;
+            if (i < r.rot) {
+                const bool first = i < half;
+                const int pair = first ? i : i - half;
+                const float2 t = cs[pair];
+                const float p = load1<RT>(base, row + (first ? i + half : pair));
+                y[k] = first ? y[k] * t.x - p * t.y : p * t.y + y[k] * t.x;
             }
         }
     }
-    return make_float4(y[0], y[1], y[2], y[3]);
 }
 
 // ---------------------------------------------------------------------------

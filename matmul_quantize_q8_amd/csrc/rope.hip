@@ -3,7 +3,8 @@
 //
 // One workgroup takes one token and, where there are few tokens, a part of its
 // heads: the token's rot/2 cosines and sines are computed once, in f64, into
-// LDS, and every wave then turns whole rows, four values a lane.  A wave loads
+// LDS, and every wave then turns whole rows, 16 bytes a lane (8 of
+// 16-bit rows whose length is no multiple of eight).  A wave loads
 // the rows it works on before it stores any of them, so y may be x.
 #include "kv_layout.h"
 
@@ -11,7 +12,7 @@ namespace qmm {
 
 constexpr int kRopeThreads = 256;
 
-template <int RT>
+template <int RT, int V>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(Rope r, const void *x, void *y, const int32_t *positions,
                                                        int H, int D, Strides xs, Strides ys) {
     __shared__ float2 cs[kMaxHeadDim / 2];
@@ -19,17 +20,22 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(Rope r, const void *x, vo
     rope_table(r, positions[t], cs, threadIdx.x, kRopeThreads);
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int quads = D >> 2, per_wave = 64 / quads, sub = lane / quads, n = 4 * (lane - sub * quads);
+    const int lanes = D / V, per_wave = 64 / lanes, sub = lane / lanes, n = V * (lane - sub * lanes);
     if (sub >= per_wave) return;
     const int step = gridDim.y * (kRopeThreads / 64) * per_wave;
     int h = (blockIdx.y * (kRopeThreads / 64) + wave) * per_wave + sub;
+    float v[V];
     for (; h + step < H; h += 2 * step) {                 // two rows' loads in flight: neither store may pass them
-        const float4 v = rotate4<RT>(x, t * xs.token + h * xs.head, n, r, cs);
-        const float4 w = rotate4<RT>(x, t * xs.token + (h + step) * xs.head, n, r, cs);
-        store4<RT>(y, t * ys.token + h * ys.head + n, v);
-        store4<RT>(y, t * ys.token + (h + step) * ys.head + n, w);
+        float w[V];
+        rotate<RT, V>(x, t * xs.token + h * xs.head, n, r, cs, v);
+        rotate<RT, V>(x, t * xs.token + (h + step) * xs.head, n, r, cs, w);
+        store_row<RT, V>(y, t * ys.token + h * ys.head + n, v);
+        store_row<RT, V>(y, t * ys.token + (h + step) * ys.head + n, w);
     }
-    if (h < H) store4<RT>(y, t * ys.token + h * ys.head + n, rotate4<RT>(x, t * xs.token + h * xs.head, n, r, cs));
+    if (h < H) {
+        rotate<RT, V>(x, t * xs.token + h * xs.head, n, r, cs, v);
+        store_row<RT, V>(y, t * ys.token + h * ys.head + n, v);
+    }
 }
 
 // Parts of a token's rows: as many workgroups as give the chip four a compute
@@ -41,11 +47,13 @@ int row_parts(int64_t T, int64_t rows, int rows_per_workgroup) {
 
 hipError_t launch_rope(int rt, Rope r, const void *x, void *y, const int32_t *positions, int64_t T, int H, int D,
                        Strides xs, Strides ys, hipStream_t st) {
-    const dim3 grid((unsigned)T, (unsigned)row_parts(T, H, kRopeThreads / 64 * (64 / (D / 4))));
+    const bool wide = row_values(rt) == 8 && D % 8 == 0;
+    const dim3 grid((unsigned)T, (unsigned)row_parts(T, H, kRopeThreads / 64 * (64 / (D / (wide ? 8 : 4)))));
     void *args[] = {(void *)&r, (void *)&x, (void *)&y, (void *)&positions, (void *)&H, (void *)&D,
                     (void *)&xs, (void *)&ys};
-    const void *k = rt == R_F32 ? (const void *)k_rope<R_F32> : rt == R_F16 ? (const void *)k_rope<R_F16>
-                                                                            : (const void *)k_rope<R_BF16>;
+    const void *k = rt == R_F32   ? (const void *)k_rope<R_F32, 4>
+                    : rt == R_F16 ? (wide ? (const void *)k_rope<R_F16, 8> : (const void *)k_rope<R_F16, 4>)
+                                  : (wide ? (const void *)k_rope<R_BF16, 8> : (const void *)k_rope<R_BF16, 4>);
     return hipLaunchKernel(k, grid, dim3(kRopeThreads), args, 0, st);
 }
 
