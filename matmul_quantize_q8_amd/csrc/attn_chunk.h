@@ -4,8 +4,8 @@
 // One pass over the cache with the running maximum m and sum l of the softmax.
 // The sequence is cut into chunks of positions; a workgroup takes one chunk of
 // one key head for up to 16 of its query heads, and its four waves take tiles
-// of 32 positions in turn.  A wave works alone: no LDS and no barrier until its
-// last tile.  Per tile, with matrix instructions of 16 x 16 x 32 (f16, f32 sums):
+// of 32 or 64 positions in turn.  A wave works alone, with no barrier until its
+// last tile; only the queries and the tile's scales pass through LDS.  Per tile, with matrix instructions of 16 x 16 x 32 (f16, f32 sums):
 //
 //   S[position][head] = K q   A = 16 key rows, B = the query heads; one per
 //                             block of 32 values, its result times the block's
@@ -19,6 +19,11 @@
 // the maximum.  Codes are exact in f16; queries and weights enter as two f16
 // each (the value and what its rounding left: 22 bits), so a product keeps
 // f32's accuracy to 2^-21.
+//
+// What bounds it: memory in large unquantized caches (32 sequences of 32 heads of
+// 128, f16, 1.46 GB: 245 us, 6.0 TB/s); the vector unit and the wait for the first
+// loads in quantized ones, whose every code takes 1.1 to 1.3 instructions to become
+// an operand (131072 positions q4_0, 151 MB: 34 us, 4.5 TB/s).
 //
 // The partial results of several chunks are joined by a second launch (attn_decode.hip).
 #pragma once
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
     int pages = 0;                              // lane i: the page of the i-th group of this wave's next 64 / GR tiles
     const uint8_t *kside[GR];                   // the tile's groups: keys' side of the page and place in it
     int place[GR];
-    bool bad = false;
+    bool bad = false, whole = false;
     uint32_t kx[GR][LW], vx[GR][LW], ks[SR], vs[SR];
     const auto look_up = [&](int tile) {
         const int t = from + (tile + lane / GR * kAttnWaves) * kTile + lane % GR * kGroup;
@@ -267,10 +272,8 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
             asm volatile("" : "+v"(pages));     // waited for here, not at every tile's readlane
         }
         bad = false;
-#pragma unroll
-        for (int j = 0; j < GR; ++j) {
-            // a group past the end is not looked up: the first is read again and not used
-            const int t0 = from + tile * kTile, t = t0 + j * kGroup < to ? t0 + j * kGroup : t0;
+        const int t0 = from + tile * kTile;
+        const auto group_at = [&](int j, int t) {
             int p = __builtin_amdgcn_readlane(pages, GR * (count % (64 / GR)) + (t != t0 ? j : 0));
             if (!a.c.has_page(p)) {
                 bad = true;
@@ -278,21 +281,42 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
             }
             kside[j] = a.c.page_at(p, side) + 2 * kv * side;
             place[j] = t & (page - 1);
+        };
+        group_at(0, t0);
+        whole = place[0] + kTile <= page;
+        if (!whole) {
+#pragma unroll
+            for (int j = 1; j < GR; ++j)        // a group past the end is not looked up: the first is read again and not used
+                group_at(j, t0 + j * kGroup < to ? t0 + j * kGroup : t0);
         }
     };
     const auto load = [&](bool values, uint32_t(&x)[GR][LW], uint32_t(&sc)[SR]) {
         const int64_t off = values ? side : 0;
+        const uint8_t *const codes = kside[0] + off + (place[0] >> 4) * K::kGroupBytes;
+        const uint8_t *const first = kside[0] + off + K::scale_byte(page, place[0]);
+        if (whole) {                            // the tile lies in one page: its codes and its scales in one piece each
 #pragma unroll
-        for (int j = 0; j < GR; ++j)
+            for (int j = 0; j < GR; ++j) load_codes<F, NB>(codes + j * K::kGroupBytes, lane, x[j]);
+            if constexpr (kScaled) {
+#pragma unroll
+                for (int k = 0; k < SR; ++k)
+                    if (SW % 64 == 0 || lane + 64 * k < SW)
+                        sc[k] = *reinterpret_cast<const uint32_t *>(first + 4 * (lane + 64 * k));
+            }
+            return;
+        }
+        load_codes<F, NB>(codes, lane, x[0]);
+#pragma unroll
+        for (int j = 1; j < GR; ++j)
             load_codes<F, NB>(kside[j] + off + (place[j] >> 4) * K::kGroupBytes, lane, x[j]);
         if constexpr (kScaled) {
 #pragma unroll
             for (int k = 0; k < SR; ++k) {
                 const int i = lane + 64 * k, j = i / (8 * NB);
-                const uint8_t *p = kside[0] + off + K::scale_byte(page, place[0]);
+                const uint8_t *p = first;
 #pragma unroll
                 for (int m = 64 * k / (8 * NB); m < GR && m <= (64 * k + 63) / (8 * NB); ++m)
-                    if (j == m) p = kside[m] + off + K::scale_byte(page, place[m]);
+                    if (m > 0 && j == m) p = kside[m] + off + K::scale_byte(page, place[m]);
                 if (SW % 64 == 0 || i < SW) sc[k] = *reinterpret_cast<const uint32_t *>(p + 4 * (i - j * 8 * NB));
             }
         }

