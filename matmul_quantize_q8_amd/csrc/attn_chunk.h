@@ -232,6 +232,7 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
     __shared__ float join[2 * (8 * NB + 2) * 64];
     __shared__ v4u queries[kQueryParts][NB][QE];
     __shared__ __attribute__((aligned(16))) uint32_t scales[kScaled ? kAttnWaves : 1][kScaled ? SW : 4];
+    __shared__ float4 extras[kAttnWaves][kTile / 4];      // what is added to a tile's scores; -inf: not seen
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4, c = n / HC;
@@ -328,12 +329,19 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
             if (SW % 64 == 0 || lane + 64 * k < SW) sc[lane + 64 * k] = x[k];
         __builtin_amdgcn_wave_barrier();
     };
+    float mask = 0.0f;                          // lane i: the mask at the tile's position i
+    const auto load_mask = [&](int tile) {      // before the keys, so that no wait is added
+        const int t = from + tile * kTile + lane;
+        if (a.mask && lane < kTile && t < to) mask = a.mask[b * a.mask_stride + t];
+    };
+    float4 *const extra = extras[wave];
     look_up(wave);
     asm volatile("" : "+v"(pages));             // and the queries with them: no wait for them reaches past the tile's loads
 #pragma unroll
     for (int k = 0; k < 2 * NB; ++k) asm volatile("" : "+v"(qx[k >> 1][k & 1].x));
     if (wave < ntiles) {
         locate(wave, 0);
+        load_mask(wave);
         load(false, kx, ks);
         load(true, vx, vs);
     }
@@ -393,7 +401,7 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
     const auto step = [&](int tile, auto last) {
         constexpr bool more = !decltype(last)::value;
         const int t0 = from + tile * kTile;
-        const bool was_bad = bad;
+        const bool was_bad = bad, masked = a.mask || t0 < lo || t0 + kTile > to;
         ++count;
 
         // scores of positions t0 + 16 (COLS j + c) + 4 g + i
@@ -423,8 +431,15 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][i] = z[i];
         }
+        if (masked && lane < kTile) {           // the lowest f32 stays finite in log2 units, NaN stays NaN
+            const float y = mask * kLog2e;
+            reinterpret_cast<float *>(extra)[lane] = t0 + lane < lo || t0 + lane >= to || mask == -INFINITY ? -INFINITY
+                                                     : y < -FLT_MAX ? -FLT_MAX : y;
+        }
+        __builtin_amdgcn_wave_barrier();
         if constexpr (more) {
             locate(tile + kAttnWaves, count);
+            load_mask(tile + kAttnWaves);
             load(false, kx, ks);
         }
         if (a.softcap > 0.0f) {
@@ -439,30 +454,29 @@ __global__ __launch_bounds__(kAttnThreads, (F == KV_F16 && NB == 8 && RT == R_F3
 #pragma unroll
             for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] = NAN;
         }
-        if (a.mask || t0 < lo || t0 + kTile > to) {   // some positions may not be seen: whatever they hold is dropped
-            const auto extra = [&](int t) {           // what the mask adds; -inf: not seen
-                if (t < lo || t >= to) return -INFINITY;
-                if (!a.mask) return 0.0f;
-                const float x = a.mask[b * a.mask_stride + t], y = x * kLog2e;
-                return x == -INFINITY ? x : y < -FLT_MAX ? -FLT_MAX : y;    // the lowest f32 stays finite, NaN stays NaN
-            };
+        if (masked) {                           // some positions may not be seen: whatever they hold is dropped
 #pragma unroll
-            for (int k = 0; k < 4 * NS; ++k) {
-                const int j = k >> 2, i = k & 3;
-                const float x = extra(t0 + (COLS * j + c) * kGroup + 4 * g + i);
-                s[j][i] = x == -INFINITY ? -INFINITY : s[j][i] + x;
-                if constexpr (!kScaled) {
+            for (int j = 0; j < NS; ++j) {
+                const float4 v = extra[(COLS * j + c) * (kGroup / 4) + g];
+                const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk)
-                        if (x == -INFINITY) vx[j][i * NB + blk] = 0u;
+                for (int i = 0; i < 4; ++i) {
+                    s[j][i] = x[i] == -INFINITY ? -INFINITY : s[j][i] + x[i];
+                    if constexpr (!kScaled) {
+#pragma unroll
+                        for (int blk = 0; blk < NB; ++blk)
+                            if (x[i] == -INFINITY) vx[j][i * NB + blk] = 0u;
+                    }
                 }
             }
-            if constexpr (kScaled) {                  // codes are finite, scales need not be
+            if constexpr (kScaled) {            // codes are finite, scales need not be
+                const float *const x = reinterpret_cast<const float *>(extra);
 #pragma unroll
                 for (int k = 0; k < SR; ++k) {
                     const int e = 2 * (lane + 64 * k);
-                    if (extra(t0 + e / NB) == -INFINITY) vs[k] &= 0xffff0000u;
-                    if (extra(t0 + (e + 1) / NB) == -INFINITY) vs[k] &= 0x0000ffffu;
+                    if (SW % 64 != 0 && e >= 2 * SW) continue;
+                    if (x[e / NB] == -INFINITY) vs[k] &= 0xffff0000u;
+                    if (x[(e + 1) / NB] == -INFINITY) vs[k] &= 0x0000ffffu;
                 }
             }
         }
