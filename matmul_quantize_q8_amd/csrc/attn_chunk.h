@@ -5,13 +5,14 @@
 // The sequence is cut into chunks of positions; a workgroup takes one chunk of
 // one key head for up to 16 of its query heads, and its four waves take tiles
 // of 32 or 64 positions in turn.  A wave works alone, with no barrier until its
-// last tile; only the queries and the tile's scales pass through LDS.  Per tile, with matrix instructions of 16 x 16 x 32 (f16, f32 sums):
+// last tile; only the queries and the tile's scales and mask pass through LDS.
+// Per tile, with matrix instructions of 16 x 16 x 32 (f16, f32 sums):
 //
 //   S[position][head] = K q   A = 16 key rows, B = the query heads; one per
 //                             block of 32 values, its result times the block's
 //                             scale, so that codes enter as small integers;
 //   O[value][head] += V^T w   A = 16 values of 32 positions, B = the weights
-//                             exp(S - m), times the positions' block scales.
+//                             2^(S - r), times the positions' block scales (r: below).
 //
 // The cache's byte order makes both A operands a lane's own loaded bytes (the
 // group's lane (g, r) is the wave's lane 16 g + r), and S comes out of the
@@ -21,9 +22,9 @@
 // f32's accuracy to 2^-21.
 //
 // What bounds it: memory in large unquantized caches (32 sequences of 32 heads of
-// 128, f16, 1.46 GB: 245 us, 6.0 TB/s); the vector unit and the wait for the first
-// loads in quantized ones, whose every code takes 1.1 to 1.3 instructions to become
-// an operand (131072 positions q4_0, 151 MB: 34 us, 4.5 TB/s).
+// 128, f16, 1.46 GB: 250 us, 5.9 TB/s); the vector unit and the wait for the first
+// loads in quantized ones, whose every code takes about one vector instruction to become
+// an operand (131072 positions q4_0, 151 MB: 33 us, 4.6 TB/s).
 //
 // The partial results of several chunks are joined by a second launch (attn_decode.hip).
 #pragma once

@@ -7,8 +7,8 @@
 // whose length is no multiple of eight).  A wave loads the rows it works on
 // before it stores any of them, so y may be x.
 //
-// Bound by memory: 4096 tokens of 32 heads of 128 in bf16 (67 MB) take 15.5 us,
-// 4.3 TB/s of the 4.9 of a large copy; one token of 40 heads 2.5 us, a launch.
+// Bound by memory: 4096 tokens of 32 heads of 128 in bf16 (67 MB) take 16 us,
+// 4.2 TB/s of the 4.9 of a large copy; one token of 40 heads 2.5 us, a launch.
 #include "kv_layout.h"
 
 namespace qmm {
