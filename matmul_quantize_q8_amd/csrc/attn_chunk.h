@@ -211,20 +211,26 @@ constexpr int attn_cols(int group) { return group <= 4 ? 4 : group <= 8 ? 2 : 1;
 
 // A lane's bytes of four groups fit its registers beside the accumulators.
 template <int F, int NB> constexpr bool kFourColumns = Kv<F, NB>::L <= 48;
-// Groups of 16 positions in a wave's tile.
+// Groups of 16 positions in a wave's tile: four where a lane's bytes of them and the
+// accumulators fit its registers (9 and more heads a key head, q8_0 of 96 values:
+// 2980 GB/s with two, 3300 with four; q4_0 of 128 2625 and 2800, of 192, which
+// spills, 2300 and 2130).
 template <int F, int NB, int COLS>
-constexpr int kTileGroups = COLS == 4 || Kv<F, NB>::L <= (COLS == 2 ? 24 : NB <= 3 ? 16 : 0) ? 4 : 2;
+constexpr int kTileGroups = COLS == 4 || Kv<F, NB>::L <= (COLS == 2 || NB <= 4 ? 24 : 0) ? 4 : 2;
 
-// Waves a SIMD, which set the registers a wave has: three, except where 6 to 16
+// Waves a SIMD, which set the registers a wave has: three, except where 6 to 30
 // live values do not fit them.  Those are four columns' groups of 32 bytes a lane
 // (q8_0 of 128 values, one head a key head: 3850 GB/s at three, 4220 at two; 16-bit
-// rows 3940, 4220), f32 rows with two columns' groups of 16 bytes and more (8 heads a
-// key head: q4_0 of 128 values 2735, 3260; q8_0 of 96 3490, 3680) and rows of 192
-// values and more.  One wave for 256 f16 values with f32 rows.
+// rows 3940, 4220), tiles of four groups of 16 bytes and more, with two columns'
+// groups only for f32 rows (8 heads a key head: q4_0 of 128 values 2735, 3260;
+// q8_0 of 96 3490, 3680), and rows of 192 values and more.  One wave for 256 f16
+// values with f32 rows.
 template <int F, int NB, int RT, int COLS>
-constexpr int kAttnOccupancy =
-    F == KV_F16 && NB == 8 && RT == R_F32 ? 1
-    : NB >= 6 || (COLS == 4 && Kv<F, NB>::L >= 32) || (RT == R_F32 && COLS == 2 && NB >= 3 && Kv<F, NB>::L >= 16) ? 2 : 3;
+constexpr bool kTwoWaves = NB >= 6 || (COLS == 4 && Kv<F, NB>::L >= 32) ||
+                           (NB >= 3 && Kv<F, NB>::L >= 16 && kTileGroups<F, NB, COLS> == 4 &&
+                            (COLS == 1 || (COLS == 2 && RT == R_F32)));
+template <int F, int NB, int RT, int COLS>
+constexpr int kAttnOccupancy = F == KV_F16 && NB == 8 && RT == R_F32 ? 1 : kTwoWaves<F, NB, RT, COLS> ? 2 : 3;
 
 template <int F, int NB, int RT, int COLS>
 __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) void k_attn_chunk(AttnArgs a) {
