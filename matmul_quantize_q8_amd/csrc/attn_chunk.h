@@ -511,8 +511,11 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
 #pragma unroll
         for (int k = 1; k < 4 * NS; ++k) top = fmaxf(top, s[k >> 2][k & 3]);
         top = max_rows(top);
-        if (__any(top > r + most)) {
-            const float next = fmaxf(r, top - under);
+        if (__any(top - r > most)) {
+            // Where an f32 step is 16 (masks of -1e8) top - 8 may come out as top - 16, whose
+            // weight of 2^16 is no f16: the reference is then the largest score itself.
+            float next = fmaxf(r, top - under);
+            next = top - next > most ? top : next;
             const float alpha = r == next ? 1.0f : exp2_fast(r - next);
             r = next;
             l *= alpha;
