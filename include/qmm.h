@@ -445,9 +445,12 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, voi
  * sequence whose length is outside [0, max_len], or with a page number outside
  * [0, n_pages) under a position that lens and window leave, gives NaN (no read
  * outside the cache).  Scores, weights and sums are f32; products run on f16
- * matrix instructions with both factors exact or split into two f16 parts
- * (22 bits).  Results do not depend on what runs beside the call: sums are
- * joined in a fixed order.
+ * matrix instructions with both factors exact or split into two f16 parts: 22
+ * bits of an f32 query and of a weight times its value block's scale, whatever
+ * the values' magnitude.  A product that is small beside others is off by up to
+ * 2^-26 of the largest product of a weight and a scale before it (f16 caches:
+ * 2^-22 of the largest weight of its 32 or 64 positions).  Results do not depend
+ * on what runs beside the call: sums are joined in a fixed order.
  *   q, out : rows [B][Hq][D], Hq a multiple of H.
  *   pages  : int32 [B][pages_stride], device: page numbers of positions 0..page-1,
  *            page.., as many as max_len needs; entries past a sequence are not read.

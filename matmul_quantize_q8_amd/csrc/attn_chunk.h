@@ -38,7 +38,7 @@ namespace qmm {
 
 constexpr int kAttnThreads = 256, kAttnWaves = 4;
 constexpr int kHeadTile = 16;                   // query heads of a workgroup
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eRest = 1.92596299e-8f;     // log2 e in two parts
 constexpr int kDppRowRor4 = 0x124;              // row_ror:4: lane i of 16 reads lane (i - 4) mod 16
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
@@ -192,13 +192,79 @@ __device__ __forceinline__ void value_words(const uint32_t (&x)[Kv<F, NB>::L / 4
 // ---------------------------------------------------------------------------
 // One chunk
 // ---------------------------------------------------------------------------
-// Scores are kept in log2 units.  A wave's weights are 2^(s - r) for a reference
-// r that lies kWeightBits under the largest score it was set by.  The reference is moved (which
-// multiplies every accumulator) only when a score passes that one by kSlackBits:
-// weights, times value scales below 2, stay inside f16 (2^(8 + 6 + 1) = 32 768),
-// and small ones keep their low parts out of its subnormals.  Tiles with a value
-// scale of 2 and more (values beyond 254) make the wave keep r at the maximum.
-constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f;
+// Scores s are in log2 units.  A column's weights are p = 2^(s - r) for a reference r
+// that lies kWeightBits under the largest score it was set by; r is moved (which
+// multiplies every accumulator) when a score passes that one by kSlackBits.
+//   What becomes two halves is p times its block's scale.  Two halves hold a product to
+// 2^-22 of itself only above 2^-3: below, the low half is an f16 subnormal, and the
+// error 2^-25 whatever the product.  So scales are staged times 2^lift (exact), and a
+// tile of a quantized cache is common when they then all lie in [2^-7, 2), which two bits
+// of a half tell: products stay below 2^(8 + 6 + 1), and a column's largest so far is
+// above 1.
+//   Other tiles (values of another magnitude, blocks of zeros) and those that follow get a
+// reference rp of their own for the products, p 2^(r - rp), until r serves again: with e =
+// log2 of a position's largest lifted scale, the largest s + e is kept between kLeastBits
+// and kMostBits over rp, and moving rp multiplies the accumulators.  rp falls at most
+// kReachBits under r, and a position without scales counts as kNoScale: sums stay in f32's
+// range.  In f16 caches e is 0, and a tile is uncommon when some column's largest score is
+// more than kSunkBits under r (it follows a position whose score exceeds all others by far).
+//   (Without lift and rp results lost 2e-5 with q8_0 values of 1e-3, 4e-4 with values of
+// 1e-4, and every digit beside a position of zero values whose score lay 16 above the rest.
+// The price: 0 to 2 % with q8_0 caches, 2 to 6 % with q4_0 ones.  With rp and e in every
+// tile it was 2 to 12 %; with a loop of their own for the uncommon tiles registers spilled,
+// and it was 5 to 35 %.)
+constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f, kSunkBits = 3.0f;
+constexpr float kMostBits = 15.0f, kSetBits = 12.0f, kLeastBits = 8.0f, kReachBits = 56.0f, kNoScale = -40.0f;
+constexpr uint32_t kScaleBits = 0x60006000u, kCommonScale = 0x20002000u;
+// The lift a wave starts with: blocks whose largest value is in [0.06, 16) are common ones.
+template <int F> constexpr int kFirstLift = F == KV_Q8_0 ? 4 : 0;
+constexpr int kMostLift = 15;                   // 2^lift is an f16
+constexpr __host__ __device__ uint32_t two_halves(int e) {      // of 2^e
+    return (e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24)) * 0x10001u;
+}
+
+// A whole number at most `bits` under `top`, where the next reference is put: sums are
+// then scaled exactly.  Where an f32 step is 16 (masks of -1e8) the difference is 16 or
+// 0, and a weight of 2^16 is no f16: the reference is then `top` itself.
+__device__ __forceinline__ float under(float top, float bits) {
+    const float x = floorf(top - bits);
+    return top - x > kMostBits ? top : x;
+}
+
+// ln(2^r l) for a whole r: l = m 2^k, m near 1, and r + k is exact, so the result carries
+// one rounding of its own size.
+__device__ __forceinline__ float log_sum(float r, float l) {
+    if (l == 0.0f) return -INFINITY;
+    int k;
+    float m = frexpf(l, &k);
+    if (m < 0.70710678f) {
+        m *= 2.0f;
+        --k;
+    }
+    const float n = r + (float)k;
+    return fmaf(n, 0.693147182464599609375f, fmaf(n, -1.904654323148236e-9f, logf(m)));   // ln 2 in two parts
+}
+
+// e of position t of a tile whose scales are at sc; an infinite or NaN scale counts as the largest finite.
+template <int NB>
+__device__ __forceinline__ float scale_log2(const uint32_t *sc, int t) {
+    uint32_t top = 0;
+    if constexpr (NB % 2) {
+#pragma unroll
+        for (int k = t * NB; k < (t + 1) * NB; ++k) top = max(top, sc[k >> 1] >> (16 * (k & 1)) & 0x7fffu);
+    } else {
+        constexpr int B = NB == 6 ? 4 : 2 * NB;
+        const uint8_t *d = reinterpret_cast<const uint8_t *>(sc + t * (NB / 2));
+#pragma unroll
+        for (int u = 0; u < 2 * NB / B; ++u) {
+            const Unit<B> v = *reinterpret_cast<const Unit<B> *>(d + u * B);
+#pragma unroll
+            for (int i = 0; i < B / 4; ++i) top = max(top, max(v.w[i] & 0x7fffu, v.w[i] >> 16 & 0x7fffu));
+        }
+    }
+    top = min(top, 0x7bffu);
+    return top ? __builtin_amdgcn_logf(f16_bits_to_f32(top)) : kNoScale;
+}
 
 // Query heads of a key head fill the 16 columns of the score product only when
 // there are more than eight.  With fewer, COLS = 2 or 4 groups of positions share
@@ -365,7 +431,7 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
     }
 
     // The queries: scaled by a power of two to below 2^8, split in two f16, in LDS.
-    float unit;
+    float to_score, rest;                       // of the products: the score is their sum times it (or tanh's argument)
     {
         float x[NB][8], top = 0.0f;
 #pragma unroll
@@ -380,8 +446,17 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
         }
         top = max_rows(top);
         const int e = top > 0.0f && top < INFINITY ? min(max(7 - ilogbf(top), -120), 120) : 0;
-        const float up = ldexpf(1.0f, e);
-        unit = ldexpf(a.scale, -e) / kCodeUnit<F>;    // of the products: the score's natural units
+        const float up = copysignf(ldexpf(1.0f, e), a.scale), unit = ldexpf(fabsf(a.scale), -e) / kCodeUnit<F>;
+        if (a.softcap > 0.0f) {
+            to_score = unit / a.softcap, rest = 0.0f;
+        } else {                                // unit * log2 e in two parts, neither negative: -inf stays -inf
+            to_score = unit * kLog2e;
+            rest = fmaf(unit, kLog2e, -to_score) + unit * kLog2eRest;
+            if (rest < 0.0f) {
+                to_score = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, to_score) - 1u);
+                rest = fmaf(unit, kLog2e, -to_score) + unit * kLog2eRest;
+            }
+        }
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
             if ((blk & (kAttnWaves - 1)) != wave) continue;   // every wave has them all and writes its share
@@ -407,19 +482,22 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
     for (int j = 0; j < COLS; ++j) {
         qat[j] = c == j ? g * HC + n % HC : QE - 1;
         mine[j] = c == j ? 0xffffffffu : 0u;
+        if (COLS > 1) asm volatile("" : "+v"(mine[j]));     // stays a mask: as conditions they hold scalar registers, which spill
     }
 
     v4f o[NB][2];
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) o[blk][0] = o[blk][1] = v4f{0.f, 0.f, 0.f, 0.f};
-    float r = -INFINITY, l = 0.0f, under = kWeightBits, most = kWeightBits + kSlackBits;
+    float r = -INFINITY, rp = -INFINITY, l = 0.0f;
 
-    const float capped = a.softcap > 0.0f ? unit / a.softcap : 0.0f;
-    int count = 0;
+    int count = 0, lift = kFirstLift<F>;
+    uint32_t factor = two_halves(kFirstLift<F>);
+    uint64_t apart = 0;                         // the lanes whose column's rp is not its r
     const auto step = [&](int tile, auto last) {
         constexpr bool more = !decltype(last)::value;
         const int t0 = from + tile * kTile;
         const bool was_bad = bad, masked = a.mask || t0 < lo || t0 + kTile > to;
+        const bool finished = masked || a.softcap > 0.0f;       // s holds scores, not the products' sums they come from
         ++count;
 
         // scores of positions t0 + 16 (COLS j + c) + 4 g + i
@@ -463,10 +541,10 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
         if (a.softcap > 0.0f) {
 #pragma unroll
             for (int k = 0; k < 4 * NS; ++k)
-                s[k >> 2][k & 3] = a.softcap * kLog2e * tanh_f32(s[k >> 2][k & 3] * capped);
-        } else {
+                s[k >> 2][k & 3] = a.softcap * kLog2e * tanh_f32(s[k >> 2][k & 3] * to_score);
+        } else if (masked) {
 #pragma unroll
-            for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] *= unit * kLog2e;
+            for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] = fmaf(s[k >> 2][k & 3], to_score, s[k >> 2][k & 3] * rest);
         }
         if (was_bad) {
 #pragma unroll
@@ -487,53 +565,110 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
                     }
                 }
             }
-            if constexpr (kScaled) {            // codes are finite, scales need not be
+            if constexpr (kScaled) {            // codes are finite, scales need not be: a common one instead
                 const float *const x = reinterpret_cast<const float *>(extra);
+                const uint32_t least_common = two_halves(-7 - lift);
 #pragma unroll
                 for (int k = 0; k < SR; ++k) {
                     const int e = 2 * (lane + 64 * k);
                     if (SW % 64 != 0 && e >= 2 * SW) continue;
-                    if (x[e / NB] == -INFINITY) vs[k] &= 0xffff0000u;
-                    if (x[(e + 1) / NB] == -INFINITY) vs[k] &= 0x0000ffffu;
+                    if (x[e / NB] == -INFINITY) vs[k] = (vs[k] & 0xffff0000u) | (least_common & 0x0000ffffu);
+                    if (x[(e + 1) / NB] == -INFINITY) vs[k] = (vs[k] & 0x0000ffffu) | (least_common & 0xffff0000u);
                 }
             }
         }
 
-        if constexpr (kScaled) {
-            uint32_t any = 0;
+        uint32_t odd = 0u;                      // kScaleBits of scales that are not in the common range
+        const auto stage_lifted = [&] {
+            uint32_t x[SR];
 #pragma unroll
             for (int k = 0; k < SR; ++k)
-                if (SW % 64 == 0 || lane + 64 * k < SW) any |= vs[k];
-            if (__any((any & 0x40004000u) != 0)) under = most = 0.0f;
-            stage(vs);
-        }
+                x[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, vs[k]) * __builtin_bit_cast(v2h, factor));
+            stage(x);
+            odd = 0u;
+#pragma unroll
+            for (int k = 0; k < SR; ++k)
+                if (SW % 64 == 0 || lane + 64 * k < SW) odd |= x[k] ^ kCommonScale;
+        };
+        if constexpr (kScaled) stage_lifted();
+        float f = finished ? 1.0f : to_score;   // what turns s into a score
         float top = s[0][0];
 #pragma unroll
         for (int k = 1; k < 4 * NS; ++k) top = fmaxf(top, s[k >> 2][k & 3]);
-        top = max_rows(top);
-        if (__any(top - r > most)) {
-            // Where an f32 step is 16 (masks of -1e8) top - 8 may come out as top - 16, whose
-            // weight of 2^16 is no f16: the reference is then the largest score itself.
-            float next = fmaxf(r, top - under);
-            next = top - next > most ? top : next;
-            const float alpha = r == next ? 1.0f : exp2_fast(r - next);
-            r = next;
-            l *= alpha;
+        top = max_rows(top) * f;
+        const float over = top - r;
+        constexpr float kMid = 0.5f * (kWeightBits + kSlackBits - kSunkBits), kHalf = kMid + kSunkBits;
+        uint64_t uncommon = apart;              // lanes that make the tile an uncommon one; moved: or move r
+        if constexpr (kScaled) uncommon |= __builtin_amdgcn_ballot_w64((odd & kScaleBits) != 0);
+        const uint64_t moved = uncommon | __builtin_amdgcn_ballot_w64(kScaled ? over > kWeightBits + kSlackBits
+                                                                              : fabsf(over - kMid) > kHalf);
+        float base = r, sum = 0.0f;             // the exponents' subtrahend; the weights' sum of an uncommon tile
+        if (moved != 0) {
+            const bool rise = over > kWeightBits + kSlackBits;
+            const float next = rise ? under(top, kWeightBits) : r;
+            float set = next, by = 1.0f;        // rp, and what the accumulators are multiplied by beside its move
+            if constexpr (!kScaled) uncommon |= __builtin_amdgcn_ballot_w64(over < -kSunkBits && over > -kReachBits);
+            if (uncommon != 0) {
+                float most = top;
+                if constexpr (kScaled) {
+                    stage(vs);
+                    const float e = lane < kTile ? scale_log2<NB>(sc, lane) : kNoScale, largest = max_rows(max16_lanes(e));
+                    if (largest > kNoScale && fabsf(largest + (float)lift + 2.5f) > 3.5f) {      // to [2^-2, 2^-1)
+                        const int was = lift;
+                        lift = uniform(min(max(-2 - (int)floorf(largest), 0), kMostLift));
+                        factor = two_halves(lift);
+                        by = ldexpf(1.0f, lift - was);
+                    }
+                    if (lane < kTile) reinterpret_cast<float *>(extra)[lane] = e + (float)lift;
+                    __builtin_amdgcn_wave_barrier();
+                    most = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        const float4 v = extra[(COLS * j + c) * (kGroup / 4) + g];
+                        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaf(s[j][i], f, x[i]));
+                    }
+                    most = max_rows(most);
+                    stage_lifted();
+                }
+                const float over_r = most - next, over_p = most - rp;
+                if (!(over_r >= kLeastBits && over_r <= kMostBits)) {
+                    const bool move = over_p > kMostBits || (over_p < kLeastBits && most > next - kReachBits);
+                    set = move ? fmaxf(under(most, kSetBits), next - kReachBits) : rp;
+                }
+                apart = __builtin_amdgcn_ballot_w64(set != next);
+            }
+            l *= r == next ? 1.0f : exp2_fast(r - next);
+            by *= rp == set ? 1.0f : exp2_fast(rp - set);
+            r = base = next;
+            rp = set;
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    o[blk][0][i] *= alpha;
-                    o[blk][1][i] *= alpha;
+                    o[blk][0][i] *= by;
+                    o[blk][1][i] *= by;
                 }
+            if (uncommon != 0) {                // r and rp may be far apart: an exponent for each, without a rounding of s
+                const float base_r = r == -INFINITY ? 0.0f : r, base_p = rp == -INFINITY ? 0.0f : rp;
+#pragma unroll
+                for (int k = 0; k < 4 * NS; ++k) {
+                    const float x = s[k >> 2][k & 3];
+                    sum += exp2_fast(finished ? x - base_r : fmaf(x, rest, fmaf(x, f, -base_r)));
+                    s[k >> 2][k & 3] = finished ? x - base_p : fmaf(x, rest, fmaf(x, f, -base_p));
+                }
+                f = 1.0f, base = 0.0f;
+            }
         }
-        const float base = r == -INFINITY ? 0.0f : r;
-        float p[NS][4];
+        base = base == -INFINITY ? 0.0f : base;
+        float p[NS][4], total = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4 * NS; ++k) {
-            p[k >> 2][k & 3] = exp2_fast(s[k >> 2][k & 3] - base);
-            l += p[k >> 2][k & 3];
+            p[k >> 2][k & 3] = exp2_fast(fmaf(s[k >> 2][k & 3], f, -base));
+            total += p[k >> 2][k & 3];
         }
+        l += uncommon != 0 ? sum : total;
         uint32_t vd[NS][2 * NB];
         if constexpr (kScaled) {
 #pragma unroll
@@ -581,15 +716,14 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
 
     // The wave's result, then the four waves' in a fixed order: 0 + 2, 1 + 3, both.
     l = sum_rows(l);
-    if constexpr (kScaled) {
+    const float back = ldexpf(r == rp ? 1.0f : exp2_fast(rp - r), -lift) / kCodeUnit<F>;      // sums of p times the values
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
+    for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[blk][0][i] *= 1.0f / kCodeUnit<F>;
-                o[blk][1][i] *= 1.0f / kCodeUnit<F>;
-            }
-    }
+        for (int i = 0; i < 4; ++i) {
+            o[blk][0][i] *= back;
+            o[blk][1][i] *= back;
+        }
     if constexpr (COLS > 1) {                   // a head's columns: 8 lanes apart, and 4
         const auto fold = [&](auto dpp) {
             constexpr int kCtrl = decltype(dpp)::value;
@@ -652,7 +786,7 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
             const float x[2] = {o[blk][0][i] * inv, o[blk][1][i] * inv};
             store2<RT>(a.out, row + blk * 32 + 2 * (4 * g + i), x);
         }
-    if (a.lse && g == 0) a.lse[head] = (r == -INFINITY ? 0.0f : r / kLog2e) + logf(l);
+    if (a.lse && g == 0) a.lse[head] = log_sum(r, l);
 }
 
 // The first launch of a format, for the query heads of a key head that decide the columns.

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(AttnArgs a, int D) {
     const int64_t b = head / a.Hq, h = head - b * a.Hq;
     store4<RT>(a.out, b * a.os.token + h * a.os.head + 4 * quad,
                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (a.lse && tid == 0) a.lse[head] = (r == -INFINITY ? 0.0f : r) / kLog2e + logf(l);
+    if (a.lse && tid == 0) a.lse[head] = log_sum(r, l);
 }
 
 struct AttnSplit {
