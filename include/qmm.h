@@ -443,8 +443,8 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, voi
  * mask[b][t] is not -inf (below -2.3e38 mask values count as equal); nothing that the cache holds elsewhere, NaN included,
  * reaches a result.  With no position seen, out is 0 and lse is -inf.  A
  * sequence whose length is outside [0, max_len], or with a page number outside
- * [0, n_pages) under a position that lens and window leave, gives NaN (no read
- * outside the cache).  Scores, weights and sums are f32; products run on f16
+ * [0, n_pages) under a position that lens and window leave, whatever the mask
+ * hides, gives NaN (no read outside the cache).  Scores, weights and sums are f32; products run on f16
  * matrix instructions with both factors exact or split into two f16 parts: 22
  * bits of an f32 query and of a weight times its value block's scale, whatever
  * the values' magnitude.  A product that is small beside others is off by up to

@@ -496,9 +496,10 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
     const auto step = [&](int tile, auto last) {
         constexpr bool more = !decltype(last)::value;
         const int t0 = from + tile * kTile;
-        const bool was_bad = bad, masked = a.mask || t0 < lo || t0 + kTile > to;
+        const bool masked = a.mask || t0 < lo || t0 + kTile > to;
         const bool finished = masked || a.softcap > 0.0f;       // s holds scores, not the products' sums they come from
         ++count;
+        if (bad) l = NAN;                       // and stays so: a bad page is told whatever the mask hides
 
         // scores of positions t0 + 16 (COLS j + c) + 4 g + i
         float s[NS][4];
@@ -545,10 +546,6 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
         } else if (masked) {
 #pragma unroll
             for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] = fmaf(s[k >> 2][k & 3], to_score, s[k >> 2][k & 3] * rest);
-        }
-        if (was_bad) {
-#pragma unroll
-            for (int k = 0; k < 4 * NS; ++k) s[k >> 2][k & 3] = NAN;
         }
         if (masked) {                           // some positions may not be seen: whatever they hold is dropped
 #pragma unroll

@@ -1,0 +1,35 @@
+"""Decode attention on an MI355X where lengths, pages and masks meet."""
+import numpy as np
+import pytest
+
+from test_gpu_attention import FORMATS, Setup, _dev, _np, env  # noqa: F401
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("Hq,heads,dim", [(4, 2, 64), (16, 1, 128), (8, 1, 256)])
+def test_bad_page_behind_a_mask(env, fmt, Hq, heads, dim):  # noqa: F811
+    """A page number outside the cache under positions that length and window leave gives
+    NaN whatever the mask hides: all of the page, all of its tile of up to 64 positions, or
+    half of the page.  Before the window the page is not looked at."""
+    torch, _, _ = env
+    print("[case] bad page behind a mask", fmt, Hq, heads, dim, flush=True)
+    lens = [400, 400, 400, 400, 400, 30]
+    s = Setup(env, fmt, lens, Hq, heads, dim, 16, "f32", 11)
+    table = s.table.copy()
+    table[:3, 9] = [-1, s.cache.n_pages, -(1 << 31)]         # under positions 144 .. 159
+    table[5, 1] = 1 << 30                                    # under the last 14 of 30
+    s.pages = _dev(torch, table)
+    mask = np.zeros((len(lens), s.max_len), np.float32)
+    mask[0, 144:160] = -np.inf
+    mask[1, 64:256] = -np.inf
+    mask[2, 144:152] = -np.inf
+    mask[3, 144:160] = -np.inf                               # the same mask over good pages
+    mask[5, 16:30] = -np.inf
+    s.run(mask=_dev(torch, mask))
+    bad = [0, 1, 2, 5]
+    assert np.isnan(_np(s.out)[bad]).all() and np.isnan(_np(s.lse)[bad]).all()
+    s.check(mask=mask, rows=[3, 4])
+    s.run(mask=_dev(torch, mask), window=200)                # from position 200 on
+    assert np.isnan(_np(s.out)[5]).all()
+    s.check(mask=mask, rows=[0, 1, 2, 3, 4], window=200)
