@@ -440,8 +440,8 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, voi
  *   s_t = z + mask[b][t],   z = scale * q.k_t, or softcap * tanh(scale * q.k_t / softcap),
  *   out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = ln sum_t exp(s_t).
  * Position t is seen when t < lens[b], t >= lens[b] - window (window > 0) and
- * mask[b][t] is not -inf (below -2.3e38 mask values count as equal); nothing that the cache holds elsewhere, NaN included,
- * reaches a result.  With no position seen, out is 0 and lse is -inf.  A
+ * mask[b][t] is not -inf (mask values below -2.3e38 count as the lowest f32);
+ * nothing that the cache holds elsewhere, NaN included, reaches a result.  With no position seen, out is 0 and lse is -inf.  A
  * sequence whose length is outside [0, max_len], or with a page number outside
  * [0, n_pages) under a position that lens and window leave, whatever the mask
  * hides, gives NaN (no read outside the cache).  Scores, weights and sums are f32; products run on f16

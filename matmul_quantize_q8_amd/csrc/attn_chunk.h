@@ -232,9 +232,11 @@ __device__ __forceinline__ float under(float top, float bits) {
 }
 
 // ln(2^r l) for a whole r: l = m 2^k, m near 1, and r + k is exact, so the result carries
-// one rounding of its own size.
+// one rounding of its own size.  (A mask's lowest value stands at r = -FLT_MAX, though its
+// product with log2 e is below that.)
 __device__ __forceinline__ float log_sum(float r, float l) {
     if (l == 0.0f) return -INFINITY;
+    if (r == -FLT_MAX && l > 0.0f) return -FLT_MAX;
     int k;
     float m = frexpf(l, &k);
     if (m < 0.70710678f) {

@@ -33,3 +33,25 @@ def test_bad_page_behind_a_mask(env, fmt, Hq, heads, dim):  # noqa: F811
     s.run(mask=_dev(torch, mask), window=200)                # from position 200 on
     assert np.isnan(_np(s.out)[5]).all()
     s.check(mask=mask, rows=[0, 1, 2, 3, 4], window=200)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 50, 5000])
+def test_lse_of_the_lowest_mask(env, fmt, n):  # noqa: F811
+    """Where every position that is seen has the mask's lowest value, the log-sum-exp is
+    that value (ln n and the scores are far below half a step of it), the output their
+    mean; beside any other position they do not count."""
+    torch, _, _ = env
+    print("[case] lowest mask", fmt, n, flush=True)
+    low = np.finfo(np.float32).min
+    s = Setup(env, fmt, [n, n, n], 4, 2, 64, 16, "f32", n)
+    mask = np.full((3, n), low, np.float32)
+    mask[1, ::2] = -np.inf
+    mask[2, n // 2] = -5.0
+    if n == 1:
+        mask[1] = low
+    s.run(mask=_dev(torch, mask))
+    lse = _np(s.lse)
+    assert np.all(lse[:2] == low) and np.all(np.abs(lse[2]) < 100)
+    s.check(mask=mask)
