@@ -300,7 +300,8 @@ qmm_status qmm_get_rows_q5_1(const void *w, const int32_t *ids, float *out, int6
  *   data + t * token_stride + h * head_stride     (strides in elements),
  * so slices of a fused QKV product can be passed as they are.  Pointers to rows
  * and both strides are multiples of four elements (QMM_E_ALIGN otherwise);
- * strides are not negative.  Index arrays (positions, slots, pages, lens) and
+ * strides are not negative, and rows that are written do not overlap one another
+ * (QMM_E_SHAPE otherwise; rows that are read may).  Index arrays (positions, slots, pages, lens) and
  * f32 arrays need the alignment of their type.  T, B, Hq, H >= 1; T < 2^24,
  * B < 2^16, Hq <= 4096. */
 typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;

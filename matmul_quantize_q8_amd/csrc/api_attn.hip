@@ -1,6 +1,7 @@
 // C ABI of the attention operators: argument checks, launch.  Declarations and
 // contracts are in include/qmm.h.
 #include <cmath>
+#include <utility>
 
 #include "api_check.h"
 #include "kv_layout.h"
@@ -35,6 +36,24 @@ qmm_status check_rows(const void *p, int dt, int64_t T, int64_t H, int64_t D, in
     if (p == nullptr) return QMM_E_NULL;
     if (token % 4 != 0 || head % 4 != 0 || !aligned(p, 4 * row_type_bytes(dt))) return QMM_E_ALIGN;
     return QMM_OK;
+}
+
+// Rows that are written, of which no two may share an element: their offsets
+// t * token + h * head lie D and more apart.
+bool rows_apart(int64_t T, int64_t H, int64_t D, int64_t token, int64_t head) {
+    if ((T > 1 && token < D) || (H > 1 && head < D)) return false;
+    if (T == 1 || H == 1 || (H - 1) * head + D <= token || (T - 1) * token + D <= head) return true;
+    if (T < H) std::swap(T, H), std::swap(token, head);
+    for (int64_t h = 1; h < H; ++h) {                 // neither is inside a step of the other: the row before h steps, and after
+        const int64_t t = h * head / token, before = h * head - t * token;
+        if ((t < T && before < D) || (t + 1 < T && token - before < D)) return false;
+    }
+    return true;
+}
+
+qmm_status check_out(const void *p, int dt, int64_t T, int64_t H, int64_t D, int64_t token, int64_t head) {
+    const qmm_status s = check_rows(p, dt, T, H, D, token, head);
+    return s != QMM_OK ? s : rows_apart(T, H, D, token, head) ? QMM_OK : QMM_E_SHAPE;
 }
 
 bool head_dim_ok(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
@@ -91,7 +110,7 @@ qmm_status kv_write(int fmt, const qmm_rope_plan *plan, const qmm_kv_cache *cach
         if (Hq > kMaxHeads) return QMM_E_SHAPE;
         QMM_TRY(check_plan(plan, D, false, a.r));
         QMM_TRY(check_rows(q, dtype, T, Hq, D, qs.token, qs.head));
-        QMM_TRY(check_rows(q_out, dtype, T, Hq, D, qos.token, qos.head));
+        QMM_TRY(check_out(q_out, dtype, T, Hq, D, qos.token, qos.head));
         QMM_TRY(check_index(positions, 4));
     }
     QMM_TRY(check_rows(k, dtype, T, H, D, ks.token, ks.head));
@@ -119,8 +138,8 @@ qmm_status kv_read(int fmt, const qmm_kv_cache *cache, const int64_t *slots, voi
     ReadArgs a = {};
     QMM_TRY(check_cache(fmt, cache, a.c));
     if (k == nullptr && v == nullptr) return QMM_E_NULL;
-    if (k != nullptr) QMM_TRY(check_rows(k, dtype, T, cache->heads, cache->dim, ks.token, ks.head));
-    if (v != nullptr) QMM_TRY(check_rows(v, dtype, T, cache->heads, cache->dim, vs.token, vs.head));
+    if (k != nullptr) QMM_TRY(check_out(k, dtype, T, cache->heads, cache->dim, ks.token, ks.head));
+    if (v != nullptr) QMM_TRY(check_out(v, dtype, T, cache->heads, cache->dim, vs.token, vs.head));
     QMM_TRY(check_index(slots, 8));
     QMM_TRY(check_device());
     a.slots = slots;
@@ -152,7 +171,7 @@ qmm_status attn_decode(int fmt, const qmm_kv_cache *cache, const void *q, void *
     if (!(softcap >= 0.0f) || std::isinf(softcap) || std::isnan(scale)) return QMM_E_SHAPE;
     if (mask != nullptr && (mask_stride < max_len || mask_stride > kMaxBytes / 4 / B)) return QMM_E_SHAPE;
     QMM_TRY(check_rows(q, dtype, B, Hq, cache->dim, qs.token, qs.head));
-    QMM_TRY(check_rows(out, dtype, B, Hq, cache->dim, os.token, os.head));
+    QMM_TRY(check_out(out, dtype, B, Hq, cache->dim, os.token, os.head));
     QMM_TRY(check_index(pages, 4));
     QMM_TRY(check_index(lens, 4));
     if (mask != nullptr) QMM_TRY(check_index(mask, 4));
@@ -235,7 +254,7 @@ qmm_status qmm_rope(const qmm_rope_plan *plan, const void *x, void *y, int dtype
     Rope r;
     QMM_TRY(check_plan(plan, D, inverse != 0, r));
     QMM_TRY(check_rows(x, dtype, T, H, D, x_token_stride, x_head_stride));
-    QMM_TRY(check_rows(y, dtype, T, H, D, y_token_stride, y_head_stride));
+    QMM_TRY(check_out(y, dtype, T, H, D, y_token_stride, y_head_stride));
     QMM_TRY(check_index(positions, 4));
     QMM_TRY(check_device());
     return launched(launch_rope(dtype, r, x, y, positions, T, (int)H, (int)D, {x_token_stride, x_head_stride},
