@@ -102,23 +102,32 @@ def _addr(t) -> int | None:
     return t.data_ptr()
 
 
-_raw_stream = None
+_raw_device = _raw_handle = None
+
+
+def _torch_handles() -> None:
+    """The functions that give the current device and a device's current stream.
+    torch.cuda.current_stream() builds a Stream object, 2.8 us a call; the handle
+    itself takes 0.2 us."""
+    global _raw_device, _raw_handle
+    import torch
+    c = torch._C
+    torch.cuda.current_stream()                           # initializes the device
+    _raw_device = getattr(c, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_handle = getattr(c, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _current_device() -> int:
+    """The index of torch's current device."""
+    if _raw_device is None:
+        _torch_handles()
+    return _raw_device()
 
 
 def _current_stream() -> int:
-    """The current torch stream's handle.  torch.cuda.current_stream() builds a
-    Stream object for it, 2.8 us a call; the handle itself takes 0.2 us."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        c = torch._C
-        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
-            torch.cuda.current_stream()                   # initializes the device
-            handle, device = c._cuda_getCurrentRawStream, c._cuda_getDevice
-            _raw_stream = lambda: handle(device())        # noqa: E731
-        else:
-            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream      # noqa: E731
-    return _raw_stream()
+    """The handle of torch's current stream on its current device."""
+    device = _current_device()
+    return _raw_handle(device)
 
 
 def _stream(stream) -> int | None:
@@ -127,6 +136,13 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _stream_on(stream, device: int) -> int:
+    """The stream's handle; of none given, the current one of the device, which _current_device gave."""
+    if stream is None:
+        return _raw_handle(device)
+    return _stream(stream)
 
 
 def _check(name: str, st: int) -> None:
@@ -309,7 +325,7 @@ QUANTIZE_MATVEC = {"q4_0": qmm_quantize_matvec_q4_0, "q8_0": qmm_quantize_matvec
 GET_ROWS = {f: globals()["qmm_get_rows_" + f] for f in WEIGHT_FORMATS}
 
 # -- attention ------------------------------------------------------------------
-_attention.bind(_call, _stream, lib)
+_attention.bind(_call, _stream_on, lib, _current_device)
 KV_FORMATS = _attention.KV_FORMATS
 RopePlan, KVCache = _attention.RopePlan, _attention.KVCache
 kv_page_bytes, attn_workspace = _attention.kv_page_bytes, _attention.attn_workspace

@@ -3,10 +3,10 @@ cache and the attention of one new token over it (include/qmm.h).
 
 Rows are torch tensors [tokens][heads][dim] of float32, float16 or bfloat16 on
 the GPU, the values of a row contiguous, any token and head strides (so slices
-of a fused QKV product go in as they are).  Shapes, types and devices are
-checked here (ValueError); sizes, strides and alignment by the library
-(QmmError).  Nothing is copied and nothing is allocated by a call, except by
-the helpers that say so.
+of a fused QKV product go in as they are).  Shapes, types and devices (every
+tensor of a call is on the current one) are checked here (ValueError); sizes,
+strides and alignment by the library (QmmError).  Nothing is copied and nothing
+is allocated by a call, except by the helpers that say so.
 """
 from __future__ import annotations
 
@@ -53,13 +53,14 @@ def declare(L) -> None:
     L.qmm_attn_decode_workspace.restype = I64
 
 
-# Set by the package: its call, stream and library access.
-_call = _stream = _lib = None
+# Set by the package: its call, the stream of a call on a device, its library
+# access and the current device.
+_call = _stream = _lib = _current = None
 
 
-def bind(call, stream, lib) -> None:
-    global _call, _stream, _lib
-    _call, _stream, _lib = call, stream, lib
+def bind(call, stream, lib, current) -> None:
+    global _call, _stream, _lib, _current
+    _call, _stream, _lib, _current = call, stream, lib, current
 
 
 # torch, imported at the first use of it, and the row types' codes.
@@ -76,15 +77,29 @@ def _t():
     return _torch
 
 
-def _rows(name, t, shape, dtype):
+def _device(name, t) -> int:
+    """The index of a call's first tensor's device, which has to be the current one."""
+    device = t.get_device()
+    if device < 0:
+        raise _elsewhere(name, device, None)
+    if device != _current():
+        raise ValueError(f"{name}: on cuda:{device}, and the current device is cuda:{_current()}")
+    return device
+
+
+def _elsewhere(name, got, device):
+    return ValueError(f"{name}: not on the GPU" if got < 0 else f"{name}: on cuda:{got}, the call is on cuda:{device}")
+
+
+def _rows(name, t, shape, dtype, device):
     """(address, token stride, head stride) of rows of that shape and type."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     token, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the values of a row have to be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not on the GPU")
+    if t.get_device() != device:
+        raise _elsewhere(name, t.get_device(), device)
     return t.data_ptr(), token, head
 
 
@@ -103,11 +118,13 @@ def _three(name, t):
     return shape
 
 
-def _array(name, t, dtype, shape):
-    """Address of a contiguous array on the GPU."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: want a contiguous {dtype} {tuple(shape)} on the GPU, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _array(name, t, dtype, shape, device=None):
+    """Address of a contiguous array on the GPU, on the call's device if there is a call."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    on = t.get_device()
+    if on < 0 or (on != device and device is not None):
+        raise _elsewhere(name, on, device)
     return t.data_ptr()
 
 
@@ -135,18 +152,25 @@ class RopePlan:
         self.freqs = freqs
         self._c = _Plan(_array("freqs", freqs, torch.float64, (freqs.numel(),)), 2 * freqs.numel(),
                         ROPE_ORDERS[order], mscale)
-        self._p = ctypes.addressof(self._c)
+        self._p, self._device = ctypes.addressof(self._c), freqs.get_device()
+
+    def on(self, device):
+        """The C structure's address, for a call on that device."""
+        if device != self._device:
+            raise _elsewhere("plan", self._device, device)
+        return self._p
 
 
 def qmm_rope(x, y, positions, plan: RopePlan, inverse: bool = False, stream=None) -> None:
     """y = x [T][H][D] with the first rot values of every row rotated to its
     token's position (int32 [T]); inverse: by the negative angle, which takes
     the gradient of y to that of x.  y may be x."""
-    torch, shape, dtype = _t(), _three("x", x), x.dtype
-    xa, xt, xh = _rows("x", x, shape, dtype)
-    ya, yt, yh = _rows("y", y, shape, dtype)
-    _call("qmm_rope", plan._p, xa, ya, _code(dtype), _array("positions", positions, torch.int32, shape[:1]),
-          1 if inverse else 0, shape[0], shape[1], shape[2], xt, xh, yt, yh, _stream(stream))
+    torch, shape, dtype, device = _t(), _three("x", x), x.dtype, _device("x", x)
+    xa, xt, xh = _rows("x", x, shape, dtype, device)
+    ya, yt, yh = _rows("y", y, shape, dtype, device)
+    _call("qmm_rope", plan.on(device), xa, ya, _code(dtype),
+          _array("positions", positions, torch.int32, shape[:1], device), 1 if inverse else 0, shape[0], shape[1],
+          shape[2], xt, xh, yt, yh, _stream(stream, device))
 
 
 # -- cache ----------------------------------------------------------------------
@@ -180,7 +204,7 @@ class KVCache:
         self.fmt, self.data, self.page, self.heads, self.dim = fmt, data, page, heads, dim
         self.n_pages = data.numel() // size
         self._c = _Cache(data.data_ptr(), self.n_pages, page, heads, dim)
-        self._p = ctypes.addressof(self._c)
+        self._p, self._device = ctypes.addressof(self._c), data.get_device()
 
     @classmethod
     def empty(cls, fmt: str, n_pages: int, page: int, heads: int, dim: int, device="cuda"):
@@ -189,9 +213,11 @@ class KVCache:
                    page, heads, dim)
 
 
-def _of(cache, fmt):
+def _of(cache, fmt, device):
     if cache.fmt != fmt:
         raise ValueError(f"the cache holds {cache.fmt}, not {fmt}")
+    if cache._device != device:
+        raise _elsewhere("cache", cache._device, device)
     return cache._p
 
 
@@ -199,12 +225,12 @@ def _kv_write(fmt):
     name = "qmm_kv_write_" + fmt
 
     def kv_write(k, v, cache: KVCache, slots, stream=None) -> None:
-        torch, dtype, T = _t(), k.dtype, k.shape[0]
+        torch, dtype, T, device = _t(), k.dtype, k.shape[0], _device("k", k)
         shape = (T, cache.heads, cache.dim)
-        ka, kt, kh = _rows("k", k, shape, dtype)
-        va, vt, vh = _rows("v", v, shape, dtype)
-        _call(name, _of(cache, fmt), ka, va, _code(dtype), _array("slots", slots, torch.int64, (T,)), T, kt, kh, vt,
-              vh, _stream(stream))
+        ka, kt, kh = _rows("k", k, shape, dtype, device)
+        va, vt, vh = _rows("v", v, shape, dtype, device)
+        _call(name, _of(cache, fmt, device), ka, va, _code(dtype), _array("slots", slots, torch.int64, (T,), device), T,
+              kt, kh, vt, vh, _stream(stream, device))
     kv_write.__name__ = name
     kv_write.__doc__ = f"Write keys and values [T][H][D] into the slots (int64 [T]) of a {fmt} cache."
     return kv_write
@@ -214,15 +240,16 @@ def _rope_kv_write(fmt):
     name = "qmm_rope_kv_write_" + fmt
 
     def rope_kv_write(q, q_out, k, v, cache: KVCache, slots, positions, plan: RopePlan, stream=None) -> None:
-        torch, dtype, T = _t(), k.dtype, k.shape[0]
+        torch, dtype, T, device = _t(), k.dtype, k.shape[0], _device("k", k)
         shape, qshape = (T, cache.heads, cache.dim), (T, _three("q", q)[1], cache.dim)
-        qa, qt, qh = _rows("q", q, qshape, dtype)
-        oa, ot, oh = _rows("q_out", q_out, qshape, dtype)
-        ka, kt, kh = _rows("k", k, shape, dtype)
-        va, vt, vh = _rows("v", v, shape, dtype)
-        _call(name, plan._p, _of(cache, fmt), qa, oa, ka, va, _code(dtype),
-              _array("positions", positions, torch.int32, (T,)), _array("slots", slots, torch.int64, (T,)), T,
-              qshape[1], qt, qh, ot, oh, kt, kh, vt, vh, _stream(stream))
+        qa, qt, qh = _rows("q", q, qshape, dtype, device)
+        oa, ot, oh = _rows("q_out", q_out, qshape, dtype, device)
+        ka, kt, kh = _rows("k", k, shape, dtype, device)
+        va, vt, vh = _rows("v", v, shape, dtype, device)
+        _call(name, plan.on(device), _of(cache, fmt, device), qa, oa, ka, va, _code(dtype),
+              _array("positions", positions, torch.int32, (T,), device),
+              _array("slots", slots, torch.int64, (T,), device), T, qshape[1], qt, qh, ot, oh, kt, kh, vt, vh,
+              _stream(stream, device))
     rope_kv_write.__name__ = name
     rope_kv_write.__doc__ = (f"Rotate queries into q_out and write the rotated keys and the values into the slots "
                              f"of a {fmt} cache, in one launch.")
@@ -237,12 +264,12 @@ def _kv_read(fmt):
         some = k if k is not None else v
         if some is None:
             raise ValueError("neither k nor v is wanted")
-        dtype, T = some.dtype, slots.shape[0]
+        dtype, T, device = some.dtype, slots.shape[0], _device("k" if some is k else "v", some)
         shape = (T, cache.heads, cache.dim)
-        ka, kt, kh = _rows("k", k, shape, dtype) if k is not None else (None, 0, 0)
-        va, vt, vh = _rows("v", v, shape, dtype) if v is not None else (None, 0, 0)
-        _call(name, _of(cache, fmt), _array("slots", slots, torch.int64, (T,)), ka, va, _code(dtype), T, kt, kh, vt,
-              vh, _stream(stream))
+        ka, kt, kh = _rows("k", k, shape, dtype, device) if k is not None else (None, 0, 0)
+        va, vt, vh = _rows("v", v, shape, dtype, device) if v is not None else (None, 0, 0)
+        _call(name, _of(cache, fmt, device), _array("slots", slots, torch.int64, (T,), device), ka, va, _code(dtype), T,
+              kt, kh, vt, vh, _stream(stream, device))
     kv_read.__name__ = name
     kv_read.__doc__ = (f"Read the slots (int64 [T]) of a {fmt} cache back into k and v [T][H][D] (either may be None; "
                        "NaN rows for slots outside the cache).")
@@ -268,22 +295,23 @@ def _attn_decode(fmt):
 
     def attn_decode(q, out, cache: KVCache, pages, lens, max_len: int, workspace, scale=None, softcap: float = 0.0,
                     window: int = 0, mask=None, lse=None, stream=None) -> None:
-        torch, dtype = _t(), q.dtype
+        torch, dtype, device = _t(), q.dtype, _device("q", q)
         B, Hq, _ = _three("q", q)
         shape = (B, Hq, cache.dim)
-        qa, qt, qh = _rows("q", q, shape, dtype)
-        oa, ot, oh = _rows("out", out, shape, dtype)
+        qa, qt, qh = _rows("q", q, shape, dtype, device)
+        oa, ot, oh = _rows("out", out, shape, dtype, device)
         width = pages.shape[-1]
         ma, ms = None, 0
         if mask is not None:
             ms = mask.shape[-1]
-            ma = _array("mask", mask, torch.float32, (B, ms))
+            ma = _array("mask", mask, torch.float32, (B, ms), device)
         size = workspace.numel()
-        _call(name, _of(cache, fmt), qa, oa, _code(dtype), _array("pages", pages, torch.int32, (B, width)), width,
-              _array("lens", lens, torch.int32, (B,)), B, Hq, max_len,
+        _call(name, _of(cache, fmt, device), qa, oa, _code(dtype),
+              _array("pages", pages, torch.int32, (B, width), device), width,
+              _array("lens", lens, torch.int32, (B,), device), B, Hq, max_len,
               1.0 / math.sqrt(cache.dim) if scale is None else scale, softcap, window, ma, ms,
-              None if lse is None else _array("lse", lse, torch.float32, (B, Hq)), qt, qh, ot, oh,
-              _array("workspace", workspace, torch.uint8, (size,)), size, _stream(stream))
+              None if lse is None else _array("lse", lse, torch.float32, (B, Hq), device), qt, qh, ot, oh,
+              _array("workspace", workspace, torch.uint8, (size,), device), size, _stream(stream, device))
     attn_decode.__name__ = name
     attn_decode.__doc__ = (
         f"Attention of one new token of each sequence over a {fmt} cache: q, out [B][Hq][D]; pages int32 "

@@ -64,3 +64,87 @@ def test_every_output_is_checked(q, fmt, strides):  # noqa: F811
     f = getattr(L, "qmm_attn_decode_" + fmt)
     assert f(_p(cache), A, A, 0, A, 8, None, 2, 4, 256, 0.125, 0.0, 0, None, 0, None, 256, 64, *strides, A, 1 << 39,
              None) == SHAPE
+
+
+# ---------------------------------------------------------------------------
+# Devices: a second one is a stand-in, as no tensor of the calls is read
+# ---------------------------------------------------------------------------
+class OnDevice:
+    """A tensor of a shape and type that says which GPU it is on."""
+
+    def __init__(self, shape, dtype, device=0):
+        self.shape, self.dtype, self.index, self.device = tuple(shape), dtype, device, f"cuda:{device}"
+        self.is_cuda = device >= 0
+
+    def get_device(self):
+        return self.index
+
+    def stride(self):
+        s, n = [], 1
+        for x in reversed(self.shape):
+            s.insert(0, n)
+            n *= x
+        return tuple(s)
+
+    def numel(self):
+        return self.stride()[0] * self.shape[0]
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+def _calls(q, fmt):  # noqa: F811
+    """(function of named stand-ins, the stand-ins' shapes and types) of every entry point."""
+    import torch
+    f, i4, i8, u1 = torch.float32, torch.int32, torch.int64, torch.uint8
+    size = q.kv_page_bytes(fmt, 16, 2, 64)
+
+    def plan(t):
+        return q.RopePlan(t["freqs"])
+
+    def cache(t):
+        return q.KVCache(fmt, t["data"], 16, 2, 64)
+    rows, plans, caches = {"k": ((3, 2, 64), f), "v": ((3, 2, 64), f)}, {"freqs": ((32,), torch.float64)}, {
+        "data": ((4 * size,), u1)}
+    slots, positions = {"slots": ((3,), i8)}, {"positions": ((3,), i4)}
+    qs = {"q": ((3, 4, 64), f), "out": ((3, 4, 64), f)}
+    return {
+        "rope": (lambda t: q.qmm_rope(t["k"], t["v"], t["positions"], plan(t)), {**rows, **positions, **plans}),
+        "write": (lambda t: q.KV_WRITE[fmt](t["k"], t["v"], cache(t), t["slots"]), {**rows, **slots, **caches}),
+        "rope_write": (lambda t: q.ROPE_KV_WRITE[fmt](t["q"], t["out"], t["k"], t["v"], cache(t), t["slots"],
+                                                      t["positions"], plan(t)),
+                       {**rows, **qs, **slots, **positions, **plans, **caches}),
+        "read": (lambda t: q.KV_READ[fmt](cache(t), t["slots"], t["k"], t["v"]), {**rows, **slots, **caches}),
+        "read_values": (lambda t: q.KV_READ[fmt](cache(t), t["slots"], None, t["v"]),
+                        {"v": rows["v"], **slots, **caches}),
+        "attn": (lambda t: q.ATTN_DECODE[fmt](t["q"], t["out"], cache(t), t["pages"], t["lens"], 32, t["workspace"],
+                                              mask=t["mask"], lse=t["lse"]),
+                 {**qs, **caches, "pages": ((3, 2), i4), "lens": ((3,), i4), "workspace": ((4096,), u1),
+                  "mask": ((3, 32), f), "lse": ((3, 4), f)})}
+
+
+@pytest.mark.parametrize("entry", ["rope", "write", "rope_write", "read", "read_values", "attn"])
+def test_tensors_of_another_device_are_refused(q, entry, monkeypatch):  # noqa: F811
+    called = []
+    monkeypatch.setattr(q.attention, "_call", lambda *a: called.append(a))
+    monkeypatch.setattr(q.attention, "_stream", lambda *a: 0)
+    monkeypatch.setattr(q.attention, "_current", lambda: 0, raising=False)
+    f, tensors = _calls(q, "q8_0")[entry]
+
+    def run(device):
+        f({name: OnDevice(*of, device.get(name, device.get("", 0))) for name, of in tensors.items()})
+    run({})
+    assert len(called) == 1
+    for other in (1, -1):
+        for name in tensors:
+            with pytest.raises(ValueError):
+                run({name: other})
+    with pytest.raises(ValueError, match="current"):         # all on the device that is not the current one
+        run({"": 1})
+    monkeypatch.setattr(q.attention, "_current", lambda: 1)
+    assert len(called) == 1
+    run({"": 1})
+    assert len(called) == 2
