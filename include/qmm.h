@@ -462,8 +462,8 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_cache *cache, const int64_t *slots, voi
  *   mask   : f32 [B][mask_stride], mask_stride >= max_len, or NULL.
  *   lse    : f32 [B][Hq], written, or NULL.
  *   workspace : device, 16-byte aligned, at least qmm_attn_decode_workspace(...)
- *            bytes, which also suffice for any smaller B or max_len with the same
- *            heads and D; scratch, nothing in it outlives a call.  Calls that may
+ *            bytes, which also suffice for any smaller B, max_len or window (0: the
+ *            largest) with the same heads and D; scratch, nothing in it outlives a call.  Calls that may
  *            run at the same time need one each.
  * QMM_E_SHAPE also for a workspace that is too small. */
 int64_t qmm_attn_decode_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t max_len,

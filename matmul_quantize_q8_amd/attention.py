@@ -283,7 +283,7 @@ def qmm_attn_decode_workspace(B: int, Hq: int, heads: int, dim: int, max_len: in
 
 
 def attn_workspace(B: int, Hq: int, heads: int, dim: int, max_len: int, window: int = 0, device="cuda"):
-    """A new workspace for qmm_attn_decode_*, enough for smaller batches and lengths too."""
+    """A new workspace for qmm_attn_decode_*, enough for smaller batches, lengths and windows too."""
     size = qmm_attn_decode_workspace(B, Hq, heads, dim, max_len, window)
     if size == 0:
         raise ValueError(f"no attention of batch {B}, {Hq} on {heads} heads of {dim}, length {max_len}")

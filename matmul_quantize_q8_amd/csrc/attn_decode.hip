@@ -87,8 +87,8 @@ constexpr int kSplitColumns = 2 * (int)kCUs;
 constexpr int kMinChunk = 256;                  // positions: a tile of 64 for each wave
 
 static int64_t attn_span(int64_t max_len, int64_t window) {
-    // a window starts anywhere in a group of 16
-    return window > 0 && window < max_len ? window + kGroup - 1 : max_len;
+    // a window starts anywhere in a group of 16, and ends no later than the longest sequence
+    return window > 0 && window < max_len - kGroup + 1 ? window + kGroup - 1 : max_len;
 }
 static int64_t head_tiles(int64_t Hq, int64_t heads) {
     return heads * ((Hq / heads + kHeadTile - 1) / kHeadTile);

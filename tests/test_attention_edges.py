@@ -55,3 +55,14 @@ def test_lse_of_the_lowest_mask(env, fmt, n):  # noqa: F811
     lse = _np(s.lse)
     assert np.all(lse[:2] == low) and np.all(np.abs(lse[2]) < 100)
     s.check(mask=mask)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [200, 241, 242, 255, 256, 257, 2985, 2986, 2999])
+def test_windows_on_a_workspace_for_all(env, fmt, window):  # noqa: F811
+    """Windows up to a position less than the length, on a workspace made without one."""
+    print("[case] window", fmt, window, flush=True)
+    s = Setup(env, fmt, [257, 256, 3] if window < 300 else [3000, 2990, 40], 8, 2, 64, 16, "f32", window)
+    s.run(window=window)
+    s.check(window=window)

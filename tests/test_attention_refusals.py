@@ -148,3 +148,15 @@ def test_tensors_of_another_device_are_refused(q, entry, monkeypatch):  # noqa: 
     assert len(called) == 1
     run({"": 1})
     assert len(called) == 2
+
+
+def test_workspace_of_windows(q):  # noqa: F811
+    """A workspace made without a window serves calls with any: a window sees no more than all."""
+    size = q.qmm_attn_decode_workspace
+    for Hq, heads, dim in ((32, 8, 128), (14, 2, 64), (64, 1, 256)):
+        for n in (1, 255, 256, 257, 512, 1000, 4096, 131072):
+            whole = {B: size(B, Hq, heads, dim, n) for B in (1, 3, 64, 700)}
+            for w in (1, 16, n // 2, n - 241, n - 16, n - 15, n - 2, n - 1, n, n + 1, 2 * n):
+                for B in whole:
+                    if w > 0:
+                        assert 0 < size(B, Hq, heads, dim, n, w) <= whole[B], (Hq, n, w, B)
