@@ -43,7 +43,6 @@ constexpr int kDppRowRor4 = 0x124;              // row_ror:4: lane i of 16 reads
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {

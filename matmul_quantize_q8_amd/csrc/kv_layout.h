@@ -59,14 +59,6 @@ __device__ __forceinline__ void store4(void *base, int64_t i, float4 v) {
             make_uint2(pack2<RT>(v.x, v.y), pack2<RT>(v.z, v.w));
 }
 
-template <int RT>
-__device__ __forceinline__ void store1(void *base, int64_t i, float v) {
-    if constexpr (RT == R_F32)
-        static_cast<float *>(base)[i] = v;
-    else
-        static_cast<uint16_t *>(base)[i] = (uint16_t)(RT == R_F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v));
-}
-
 // ---------------------------------------------------------------------------
 // Rotation
 // ---------------------------------------------------------------------------
@@ -166,23 +158,13 @@ __device__ __forceinline__ void store8(void *base, int64_t i, const float (&x)[8
 
 // Two consecutive values; i is even.
 template <int RT>
-__device__ __forceinline__ void load2(const void *base, int64_t i, float (&x)[2]) {
-    if constexpr (RT == R_F32) {
-        const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + i);
-        x[0] = v.x, x[1] = v.y;
-    } else {
-        const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + i);
-        x[0] = RT == R_F16 ? f16_bits_to_f32(u) : __builtin_bit_cast(float, u << 16);
-        x[1] = RT == R_F16 ? f16_bits_to_f32(u >> 16) : __builtin_bit_cast(float, u & 0xffff0000u);
-    }
-}
-template <int RT>
 __device__ __forceinline__ void store2(void *base, int64_t i, const float (&x)[2]) {
     if constexpr (RT == R_F32)
         *reinterpret_cast<float2 *>(static_cast<float *>(base) + i) = make_float2(x[0], x[1]);
     else
         *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + i) = pack2<RT>(x[0], x[1]);
 }
+
 // Values n .. n+V-1 of the rotated row that starts at element `row` of `base`.
 // The pair's other value is read from memory again: the row is in the cache.
 template <int RT, int V>
