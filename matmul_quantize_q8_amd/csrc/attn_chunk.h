@@ -630,8 +630,11 @@ __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) vo
                     most = max_rows(most);
                     stage_lifted();
                 }
+                // r serves the products too where they lie high enough over it: a tile of common scales (lifted
+                // anew, or after an uncommon one) need not reach what one with blocks far below the others has to
+                const bool wide = kScaled && __builtin_amdgcn_ballot_w64((odd & kScaleBits) != 0) != 0;
                 const float over_r = most - next, over_p = most - rp;
-                if (!(over_r >= kLeastBits && over_r <= kMostBits)) {
+                if (!(over_r >= (wide ? kLeastBits : 0.0f) && over_r <= kMostBits)) {
                     const bool move = over_p > kMostBits || (over_p < kLeastBits && most > next - kReachBits);
                     set = move ? fmaxf(under(most, kSetBits), next - kReachBits) : rp;
                 }

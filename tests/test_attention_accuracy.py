@@ -102,7 +102,8 @@ def split_attention(s, code, d, fmt, weights=2, blind=False):
                 largest = np.abs(d[t:t + 64]).max()
                 if largest > 0 and abs(np.log2(largest) + lift + 2.5) > 3.5:
                     lift = int(min(max(-2 - np.floor(np.log2(largest)), 0), c["kMostLift"]))
-                by, gained = 2.0 ** (lift - was), False
+                by, gained, scales = 2.0 ** (lift - was), False, np.abs(d[t:t + 64]) * 2.0 ** lift
+                least = c["kLeastBits"] if scales.min() < 2.0 ** -7 or scales.max() >= 2.0 else 0.0
             for x in range(4):
                 o[x] = o[x] * by
             for x, i in zip(cols, at):
@@ -115,7 +116,7 @@ def split_attention(s, code, d, fmt, weights=2, blind=False):
                 if uncommon:
                     e = np.abs(dt).max(-1)
                     most = (s[i] + np.where(e > 0, np.log2(np.where(e > 0, e, 1.0)), c["kNoScale"] + lift)).max()
-                    if not c["kLeastBits"] <= most - nxt <= c["kMostBits"]:
+                    if not least <= most - nxt <= c["kMostBits"]:
                         b = most - rp[x]
                         move = b > c["kMostBits"] or (b < c["kLeastBits"] and most > nxt - c["kReachBits"])
                         to = max(np.floor(most - c["kSetBits"]), nxt - c["kReachBits"]) if move else rp[x]
