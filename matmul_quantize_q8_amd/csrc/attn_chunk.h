@@ -209,9 +209,8 @@ __device__ __forceinline__ void value_words(const uint32_t (&x)[Kv<F, NB>::L / 4
 // more than kSunkBits under r (it follows a position whose score exceeds all others by far).
 //   (Without lift and rp results lost 2e-5 with q8_0 values of 1e-3, 4e-4 with values of
 // 1e-4, and every digit beside a position of zero values whose score lay 16 above the rest.
-// The price: 0 to 2 % with q8_0 caches, 2 to 6 % with q4_0 ones.  With rp and e in every
-// tile it was 2 to 12 %; with a loop of their own for the uncommon tiles registers spilled,
-// and it was 5 to 35 %.)
+// The price: 0 to 2 % of the time, 4 to 6 % with q4_0 rows of 192 and 256 values; where
+// every tile is uncommon 5 to 12 %.)
 constexpr float kWeightBits = 8.0f, kSlackBits = 6.0f, kSunkBits = 3.0f;
 constexpr float kMostBits = 15.0f, kSetBits = 12.0f, kLeastBits = 8.0f, kReachBits = 56.0f, kNoScale = -40.0f;
 constexpr uint32_t kScaleBits = 0x60006000u, kCommonScale = 0x20002000u;
@@ -285,19 +284,16 @@ template <int F, int NB> constexpr bool kFourColumns = Kv<F, NB>::L <= 48;
 template <int F, int NB, int COLS>
 constexpr int kTileGroups = COLS == 4 || Kv<F, NB>::L <= (COLS == 2 || NB <= 4 ? 24 : 0) ? 4 : 2;
 
-// Waves a SIMD, which set the registers a wave has: three, except where 6 to 30
-// live values do not fit them.  Those are four columns' groups of 32 bytes a lane
-// (q8_0 of 128 values, one head a key head: 3850 GB/s at three, 4220 at two; 16-bit
-// rows 3940, 4220), tiles of four groups of 16 bytes and more, with two columns'
-// groups only for f32 rows (8 heads a key head: q4_0 of 128 values 2735, 3260;
-// q8_0 of 96 3490, 3680), and rows of 192 values and more.  One wave for 256 f16
-// values with f32 rows.
+// Waves a SIMD, which set the registers a wave has: three, but two for rows of 192 values
+// and more and for tiles of four groups whose lanes hold 12 bytes and more of each, which
+// spill at three or keep too few loads in flight (three and two, GB/s: q4_0 of 128 values
+// with four heads a key head and f32 rows 3240, 3430; of 96 2510, 2630; q8_0 of 96 with one
+// head and 16-bit rows 3840, 4050; rows of 64 values do not differ).  One wave for 256
+// f16 values with f32 rows.
+template <int F, int NB, int COLS>
+constexpr bool kTwoWaves = NB >= 6 || (NB >= 3 && Kv<F, NB>::L >= 12 && kTileGroups<F, NB, COLS> == 4);
 template <int F, int NB, int RT, int COLS>
-constexpr bool kTwoWaves = NB >= 6 || (COLS == 4 && Kv<F, NB>::L >= 32) ||
-                           (NB >= 3 && Kv<F, NB>::L >= 16 && kTileGroups<F, NB, COLS> == 4 &&
-                            (COLS == 1 || (COLS == 2 && RT == R_F32)));
-template <int F, int NB, int RT, int COLS>
-constexpr int kAttnOccupancy = F == KV_F16 && NB == 8 && RT == R_F32 ? 1 : kTwoWaves<F, NB, RT, COLS> ? 2 : 3;
+constexpr int kAttnOccupancy = F == KV_F16 && NB == 8 && RT == R_F32 ? 1 : kTwoWaves<F, NB, COLS> ? 2 : 3;
 
 template <int F, int NB, int RT, int COLS>
 __global__ __launch_bounds__(kAttnThreads, (kAttnOccupancy<F, NB, RT, COLS>)) void k_attn_chunk(AttnArgs a) {
