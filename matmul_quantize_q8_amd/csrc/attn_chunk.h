@@ -22,9 +22,11 @@
 // f32's accuracy to 2^-21.
 //
 // What bounds it: memory in large unquantized caches (32 sequences of 32 heads of
-// 128, f16, 1.46 GB: 250 us, 5.9 TB/s); the vector unit and the wait for the first
-// loads in quantized ones, whose every code takes about one vector instruction to become
-// an operand (131072 positions q4_0, 151 MB: 33 us, 4.6 TB/s).
+// 128, f16, 1.46 GB: 248 us, 5.9 TB/s); in quantized ones a wave's own chain, whose every
+// code takes about one vector instruction to become an operand.  There vector
+// instructions run for 26 to 50 % of a wave's time, 18 to 45 % are waits for loads and LDS, and
+// over the kernel about one wave a SIMD is left to fill them (131072 positions q4_0,
+// 151 MB: 34 us, 4.5 TB/s; 16 heads a key head 2.8).
 //
 // The partial results of several chunks are joined by a second launch (attn_decode.hip).
 #pragma once

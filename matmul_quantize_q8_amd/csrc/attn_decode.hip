@@ -80,9 +80,12 @@ struct AttnSplit {
 
 // Work is split until there are two workgroups a CU; a column (one sequence, one
 // key head, up to 16 of its query heads) is one chunk when there are as many of
-// those.  Of 128 to 2048 positions a chunk, the rule's is the fastest or within
-// 10 % of it from 300 to 131072 positions and 1 to 64 sequences; 40000 positions
-// of 8 key heads (q8_0): 24.5 us, with chunks of 256 28.1, of 1024 26.7.
+// those.  Of 128 to 2048 positions a chunk, the rule's is the fastest or within 14 %
+// of it from 1200 to 40000 positions and 1 to 64 sequences, and within 8 % in 28 of 35 such
+// cases; 40000 positions of 8 key heads (q8_0): 24.5 us, with chunks of 256 28.1, of 1024
+// 26.7.  It does not know the join's 2 to 4 us: 64 sequences of 1200 of 2 key heads of 64
+// take 13.2 us and 11.6 whole, 16 of 1200 of 8 of 128 17.5 and 15.7; and 10000 positions of
+// 8 key heads 15.2, with chunks of 384 13.5.
 constexpr int kSplitColumns = 2 * (int)kCUs;
 constexpr int kMinChunk = 256;                  // positions: a tile of 64 for each wave
 
