@@ -484,6 +484,133 @@ qmm_status qmm_attn_decode_q4_0(const qmm_kv_cache *cache, const void *q, void *
                                 float *lse, int64_t q_token_stride, int64_t q_head_stride, int64_t out_token_stride,
                                 int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---- mixture of experts: norm, routing, experts' products --------------------
+ * What a feed-forward block needs around its products, from the residual stream
+ * and back to it:
+ *   x -> qmm_rms_norm_* -> (the router's product) -> qmm_route -> qmm_experts_plan
+ *     -> qmm_experts_matmul_* (gate, up) -> qmm_glu_* -> qmm_experts_matmul_* (down)
+ *     -> qmm_experts_combine.
+ * Rows are as for attention, without heads: row t at data + t * stride, pointers
+ * and strides multiples of four elements (one row: its stride is not read).
+ * E <= 512 experts, top_k <= 64 of them for a token, T * top_k <= 2^26. */
+
+/* Residual, root-mean-square norm and quantization, in one launch:
+ *   s = x + residual, rounded to the rows' type;
+ *   y = s * (weight_offset + weight) / sqrt(mean(s^2) + eps);
+ *   xq = the Q8_0 (Q8_K) blocks of y, as qmm_quantize_q8_0 (_q8_k) makes them of
+ *        the f32 values y, except that a block with a NaN gets the scale NaN.
+ * The mean and the factors are f64, y is rounded once to f32 (and from there to
+ * the rows' type, where y is wanted).
+ *   x        : rows [T][K], K % 32 == 0 (Q8_K: % 256).
+ *   residual : rows [T][K], or NULL: s = x.
+ *   sum      : rows [T][K], written with s, or NULL.  May be x or residual itself.
+ *   weight   : f32 [K], 16-byte aligned, or NULL: ones.   weight_offset: 0, or 1
+ *              for models that store the weight less one.
+ *   xq       : T rows of blocks, written.
+ *   y        : rows [T][K], written, or NULL.  May be x or residual itself, but
+ *              not sum. */
+qmm_status qmm_rms_norm_q8_0(const void *x, const void *residual, void *sum, const float *weight, void *xq, void *y,
+                             int dtype, int64_t T, int64_t K, int64_t x_stride, int64_t residual_stride,
+                             int64_t sum_stride, int64_t y_stride, float eps, float weight_offset, void *stream);
+qmm_status qmm_rms_norm_q8_k(const void *x, const void *residual, void *sum, const float *weight, void *xq8k, void *y,
+                             int dtype, int64_t T, int64_t K, int64_t x_stride, int64_t residual_stride,
+                             int64_t sum_stride, int64_t y_stride, float eps, float weight_offset, void *stream);
+
+/* Gated activation and quantization, in one launch: xq = the blocks (as above) of
+ * act(gate) * up, computed in f32 to a few units of its last place:
+ *   QMM_GLU_SILU       g / (1 + e^-g)
+ *   QMM_GLU_GELU       g/2 (1 + erf(g / sqrt 2))
+ *   QMM_GLU_GELU_TANH  g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ *   gate, up : rows [rows][F], F % 32 == 0 (Q8_K: % 256); the halves of one
+ *              product's rows, for instance.
+ *   xq       : `rows` rows of blocks, written. */
+typedef enum { QMM_GLU_SILU = 0, QMM_GLU_GELU = 1, QMM_GLU_GELU_TANH = 2 } qmm_glu_act;
+qmm_status qmm_glu_q8_0(const void *gate, const void *up, void *xq, int dtype, int act, int64_t rows, int64_t F,
+                        int64_t gate_stride, int64_t up_stride, void *stream);
+qmm_status qmm_glu_q8_k(const void *gate, const void *up, void *xq8k, int dtype, int act, int64_t rows, int64_t F,
+                        int64_t gate_stride, int64_t up_stride, void *stream);
+
+/* Routing: the top_k experts of each token and their weights.
+ *   p = softmax(logits) over all E, or sigmoid of each;   c = p + bias;
+ *   groups > 1: experts lie in `groups` groups of E/groups; those of the
+ *     groups_kept groups with the largest sum of their group_top (1 or 2) largest
+ *     c stay;
+ *   ids = the top_k experts by c, the largest first;
+ *   weights = p of those, divided by their sum if renorm, times scale.
+ * Equal c go to the lowest index, equal groups too.  An expert whose logit (or
+ * bias) is -inf is never chosen, and where fewer than top_k can be, the rest of
+ * the ids are -1 with weight 0.  A NaN counts as larger than any number and shows
+ * in the weights.  Scores are f64, so the order is the formula's; without a bias
+ * it is the logits' own.
+ *   logits  : [T][E] in dtype, row t at t * logits_stride elements; any alignment
+ *             and stride >= 0.
+ *   bias    : f32 [E], or NULL.
+ *   ids     : int32 [T][top_k], written.    weights : f32 [T][top_k], written.
+ * top_k <= groups_kept * E/groups; groups <= 64. */
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *ids, float *weights, int64_t T,
+                     int64_t E, int64_t logits_stride, int64_t top_k, int score, int64_t groups, int64_t groups_kept,
+                     int64_t group_top, int renorm, float scale, void *stream);
+
+/* The plan of the experts' products: the (token, slot) pairs sorted by expert.
+ * One serves every product with these ids.
+ *   ids  : int32 [T][top_k], device.
+ *   plan : device, 16-byte aligned, qmm_experts_plan_bytes(T, top_k, E) bytes (0:
+ *          sizes outside the limits), written.  Plans that are in use at the same
+ *          time need a buffer each.
+ * Calls of up to 64 pairs launch nothing: their products read the ids. */
+int64_t qmm_experts_plan_bytes(int64_t T, int64_t top_k, int64_t E);
+qmm_status qmm_experts_plan(const int32_t *ids, void *plan, int64_t plan_bytes, int64_t T, int64_t top_k, int64_t E,
+                            void *stream);
+
+/* The experts' products: y[t top_k + j] = W[ids[t][j]] x, with x the activation
+ * row of the token (x_rows = T) or of the pair (x_rows = T * top_k); tolerance
+ * and formats as for the products above.  A pair whose id is outside [0, E)
+ * gets zeros (no read outside the matrices).  A result depends on its own row and
+ * matrix and on the sizes of the call, not on what other rows hold.
+ *   w    : E matrices of N rows of K/blk weight blocks, expert e's at
+ *          w + e * expert_stride bytes; expert_stride a multiple of 16
+ *          (QMM_E_ALIGN otherwise), at least one matrix.
+ *   xq   : x_rows rows of Q8_0 (K-quants: Q8_K) blocks, less than 4 GiB.
+ *   ids, plan, plan_bytes : the ids that the plan was made of, and the plan.
+ *   y    : f32 [T * top_k][N], written.
+ * N <= 2^20, T * top_k * N <= 2^36, K as for qmm_matmul_*. */
+qmm_status qmm_experts_matmul_q4_0(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q8_0(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q4_1(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q5_0(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q5_1(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q2_k(const void *w, int64_t expert_stride, const void *xq8k, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q4_k(const void *w, int64_t expert_stride, const void *xq8k, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+qmm_status qmm_experts_matmul_q6_k(const void *w, int64_t expert_stride, const void *xq8k, int64_t x_rows,
+                                   const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
+                                   int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
+
+/* out[t] = residual[t] + sum_j weights[t][j] * y[t top_k + j]: f32, in the order of
+ * j, the residual last, rounded once to the rows' type.
+ *   y        : f32 [T * top_k][N], 16-byte aligned.    weights : f32 [T][top_k].
+ *   residual : rows [T][N], or NULL.
+ *   out      : rows [T][N], written.  May be residual itself.
+ * N <= 2^20, T * top_k * N <= 2^36.  Where N is no multiple of 4, rows may have any
+ * alignment and stride. */
+qmm_status qmm_experts_combine(const float *y, const float *weights, const void *residual, void *out, int dtype,
+                               int64_t T, int64_t top_k, int64_t N, int64_t residual_stride, int64_t out_stride,
+                               void *stream);
+
 #ifdef __cplusplus
 }
 #endif

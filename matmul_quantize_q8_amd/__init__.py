@@ -9,7 +9,8 @@ computation runs in the library's HIP kernels.  There is no CPU fallback: if
 the library is missing or refuses a call, an exception is raised.
 
 The attention operators (rotary positions, paged key-value cache, decode
-attention) are in attention.py and reached from here.
+attention) are in attention.py, the mixture-of-experts operators (norm, routing,
+experts' products, gated activation) in moe.py; both are reached from here.
 
 Byte layouts (see the header): Q8_0 34 B / 32 values, Q4_0 18 B / 32,
 Q2_K 84 B / 256, Q8_K 292 B / 256.
@@ -20,6 +21,7 @@ import ctypes
 import os
 
 from . import attention as _attention
+from . import moe as _moe
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmm.so")
@@ -78,6 +80,7 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).argtypes = [P, P, P, I64, I64, I64, P]
             getattr(L, name).restype = ctypes.c_int
         _attention.declare(L)
+        _moe.declare(L)
         _lib = L
     return _lib
 
@@ -85,7 +88,7 @@ def lib() -> ctypes.CDLL:
 EXPORTS = tuple(["qmm_status_string", "qmm_abi_version", "qmm_quantize_q8_k"] +
                 ["qmm_quantize_matvec_" + f for f in FUSED_FORMATS] +
                 [p + f for p in ("qmm_quantize_", "qmm_matvec_", "qmm_matmul_", "qmm_get_rows_")
-                 for f in WEIGHT_FORMATS]) + _attention.EXPORTS
+                 for f in WEIGHT_FORMATS]) + _attention.EXPORTS + _moe.EXPORTS
 
 
 def row_bytes(fmt: str, K: int) -> int:
@@ -332,3 +335,10 @@ kv_page_bytes, attn_workspace = _attention.kv_page_bytes, _attention.attn_worksp
 KV_WRITE, ROPE_KV_WRITE, KV_READ = _attention.KV_WRITE, _attention.ROPE_KV_WRITE, _attention.KV_READ
 ATTN_DECODE = _attention.ATTN_DECODE
 globals().update({name: getattr(_attention, name) for name in _attention.EXPORTS})
+
+# -- mixture of experts -----------------------------------------------------------
+_moe.bind(_call, _stream_on, lib)
+ACT_FORMATS, GLU_ACTS, ROUTE_SCORES = _moe.ACT_FORMATS, _moe.GLU_ACTS, _moe.ROUTE_SCORES
+RMS_NORM, GLU, EXPERTS_MATMUL = _moe.RMS_NORM, _moe.GLU, _moe.EXPERTS_MATMUL
+experts_plan = _moe.experts_plan
+globals().update({name: getattr(_moe, name) for name in _moe.EXPORTS})

@@ -1,0 +1,60 @@
+// Gated activation and quantization of rows: xq = Q8(act(gate) up).
+// Bound by memory: 8 bytes read and about one written for every value.
+#include "moe.h"
+#include "q8_rows.h"
+
+namespace qmm {
+
+// In f32, each within a few units of its last place; the result is held in 8 bits.
+template <int ACT>
+__device__ __forceinline__ float activation(float g) {
+    if constexpr (ACT == G_SILU) return g / (1.0f + expf(-g));
+    if constexpr (ACT == G_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    // 0.5 (1 + tanh z) = 1 / (1 + e^(-2z))
+    const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    return g / (1.0f + expf(-z2));
+}
+
+constexpr int kGluThreads = 256;
+constexpr int64_t kGluGrid = 1 << 22;          // workgroups of a launch: a grid holds 2^32 threads
+
+template <int RT, int FMT, int ACT>
+__global__ __launch_bounds__(kGluThreads) void k_glu(GluArgs a) {
+    const int64_t row_bytes = (int64_t)(a.quads / (act_values(FMT) / 4)) * act_bytes(FMT);
+    const int64_t all = a.rows * a.quads;
+    for (int64_t base = (int64_t)blockIdx.x * kGluThreads; base < all; base += (int64_t)gridDim.x * kGluThreads) {
+        const int64_t row0 = base / a.quads;
+        const uint32_t at = (uint32_t)(base - row0 * a.quads) + threadIdx.x;
+        const int64_t row = row0 + at / (uint32_t)a.quads;
+        const int c = (int)(at % (uint32_t)a.quads);
+        if (row >= a.rows) continue;
+        const float4 g = load4<RT>(a.gate, row * a.gs + 4 * c), u = load4<RT>(a.up, row * a.us + 4 * c);
+        store_quantized<FMT>(a.xq + row * row_bytes, c,
+                             make_float4(activation<ACT>(g.x) * u.x, activation<ACT>(g.y) * u.y,
+                                         activation<ACT>(g.z) * u.z, activation<ACT>(g.w) * u.w));
+    }
+}
+
+template <int RT, int FMT>
+static hipError_t launch(int act, GluArgs a, hipStream_t st) {
+    const void *k = act == G_SILU   ? (const void *)k_glu<RT, FMT, G_SILU>
+                    : act == G_GELU ? (const void *)k_glu<RT, FMT, G_GELU>
+                                    : (const void *)k_glu<RT, FMT, G_GELU_TANH>;
+    const int64_t grid = (a.rows * a.quads + kGluThreads - 1) / kGluThreads;
+    void *args[] = {(void *)&a};
+    return hipLaunchKernel(k, dim3((unsigned)(grid < kGluGrid ? grid : kGluGrid)), dim3(kGluThreads), args, 0, st);
+}
+
+hipError_t launch_glu(int rt, int fmt, int act, const GluArgs &a, hipStream_t st) {
+    switch (rt * 2 + fmt) {
+        case R_F32 * 2 + A_Q8_0: return launch<R_F32, A_Q8_0>(act, a, st);
+        case R_F32 * 2 + A_Q8_K: return launch<R_F32, A_Q8_K>(act, a, st);
+        case R_F16 * 2 + A_Q8_0: return launch<R_F16, A_Q8_0>(act, a, st);
+        case R_F16 * 2 + A_Q8_K: return launch<R_F16, A_Q8_K>(act, a, st);
+        case R_BF16 * 2 + A_Q8_0: return launch<R_BF16, A_Q8_0>(act, a, st);
+        case R_BF16 * 2 + A_Q8_K: return launch<R_BF16, A_Q8_K>(act, a, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace qmm

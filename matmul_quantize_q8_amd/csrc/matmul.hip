@@ -64,7 +64,7 @@
 // weight rows' two scales from chunk 0 and chunk 2.  |I| <= 32*127*127 <
 // 2^22, so the bias trick holds with F = 1.5*2^23 + I and the store does not
 // rescale.
-#include "qmm_device.h"
+#include "moe.h"
 
 #include <type_traits>
 #include <utility>
@@ -185,10 +185,13 @@ __device__ __forceinline__ void each_index(std::integer_sequence<int, I...>, Fn 
 // Workgroup barrier that orders LDS accesses but does not wait for
 // outstanding vector-memory loads (the LDS-DMA copies in flight).
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-template <int WFMT, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4>
+// GROUPED: one tile of the experts' products.  M is its row count, w its
+// expert's matrix, `rows` says where its rows come from and go to.
+template <int WFMT, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4, bool GROUPED = false>
 __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restrict__ w,
                                             const uint8_t *__restrict__ xq, float *__restrict__ y, int M, int N,
-                                            int nb, int tiles_m) {
+                                            int nb, int tiles_m, const TileRows &rows = TileRows()) {
+    static_assert(!GROUPED || !SPLIT, "a tile of the experts' products has K whole");
     using namespace mm;
     using F = WF<WFMT>;
     constexpr bool Q8W = F::Q8W, Q5 = F::Q5, MIN = F::MIN;
@@ -216,7 +219,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
     constexpr int P = ksplit * G;
     const int tiles = (int)gridDim.x / ksplit;
     const int tile = (int)blockIdx.x % tiles, gpart = (int)blockIdx.x / tiles;
-    const int mt = tile % tiles_m, nt = tile / tiles_m;
+    const int mt = GROUPED ? 0 : tile % tiles_m, nt = GROUPED ? rows.nt : tile / tiles_m;
     constexpr int TBN = NARROW ? 32 * WPG : BN;          // weight rows per tile
     const int m0 = mt * TBM, n0 = nt * TBN;
     const uint32_t xrow = (uint32_t)nb * kQ80Bytes, wrow = (uint32_t)nb * F::WB;
@@ -243,9 +246,16 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
     // and block 0 a copy of the block before it, whose weight scales are
     // taken as 0 (it adds nothing).
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(xq + (int64_t)m0 * xrow), 0, (int)((uint32_t)min(M - m0, TBM) * xrow), 0x00020000);
+        (void *)(xq + (int64_t)m0 * xrow), 0, (int)(GROUPED ? rows.x_bytes : (uint32_t)min(M - m0, TBM) * xrow),
+        0x00020000);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
         (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(N - n0, TBN) * wrow), 0x00020000);
+    // the activation buffer's row of the tile's row
+    auto source = [&](int row) {
+        const int r = min(m0 + row, M - 1) - m0;
+        if constexpr (GROUPED) return (uint32_t)rows.src[r];
+        return (uint32_t)r;
+    };
     uint32_t voff[PER_WAVE];
     uint32_t m0k[PER_WAVE];   // narrow: the LDS base of each of this wave's loads
     if constexpr (!NARROW) {
@@ -254,7 +264,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
             const int q = wave + 4 * k;
             if (q < XQ) {
                 const int f = kWave * q + lane, row = f / XC, c = f - XC * row;
-                voff[k] = (uint32_t)(min(m0 + row, M - 1) - m0) * xrow + (uint32_t)xchunk(c);
+                voff[k] = source(row) * xrow + (uint32_t)xchunk(c);
             } else {
                 const int f = kWave * (q - XQ) + lane, row = f / WC, c = f - WC * row;
                 voff[k] = (uint32_t)(min(n0 + row, N - 1) - n0) * wrow + (uint32_t)F::wchunk(c);
@@ -274,7 +284,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
                 // repeat another wave's (the same bytes to the same place)
                 const int a = min(wave + WPG * k, NXL - 1);
                 const int f = min(kWave * a + lane, NBM * XC - 1), row = f / XC, c = f - XC * row;
-                voff[k] = (uint32_t)(min(m0 + row, M - 1) - m0) * xrow + (uint32_t)xchunk(c);
+                voff[k] = source(row) * xrow + (uint32_t)xchunk(c);
                 m0k[k] = (uint32_t)uniform((int)(lds0 + 1024u * a));
             } else {
                 const int f = min(kWave * (k - NA) + lane, 32 * WC - 1), row = f / WC, c = f - WC * row;
@@ -751,7 +761,9 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
                 const int m = m0 + (NARROW ? 0 : 64 * wm + 32 * i) + 8 * (r >> 2) + 4 * lh + (r & 3);
                 if (m >= M) continue;
                 // two addends on a zeroed output: the same sum in either order
-                if constexpr (SPLIT)
+                if constexpr (GROUPED)
+                    y[(int64_t)rows.pair[m] * N + n] = acc[i][j][r] * F::OUT_SCALE;
+                else if constexpr (SPLIT)
                     atomicAdd(y + (int64_t)m * N + n, acc[i][j][r] * F::OUT_SCALE);
                 else
                     y[(int64_t)m * N + n] = acc[i][j][r] * F::OUT_SCALE;
@@ -862,6 +874,45 @@ __global__ __launch_bounds__(mm::NT, 2) void k_matmul_narrow(const uint8_t *__re
     static_assert(2 * mm::WN<WFMT>::template LDS_BYTES<1> <= 160 * 1024, "two workgroups per CU");
     __shared__ __attribute__((aligned(16))) uint8_t lds[mm::WN<WFMT>::template LDS_BYTES<1>];
     matmul_body<WFMT, SPLIT, true>(lds, w, xq, y, M, N, nb, tiles_m);
+}
+
+// The experts' products: a tile of the plan and 128 weight rows of its expert to
+// a workgroup, consecutive workgroups on the same rows.
+template <int WFMT, bool NARROW>
+__global__ __launch_bounds__(mm::NT, 2) void k_experts_matmul(ExpertArgs a, int tiles_n) {
+    constexpr int LDS = NARROW ? mm::WN<WFMT>::template LDS_BYTES<1> : mm::WF<WFMT>::LDS_BYTES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+    const int chunk = (int)blockIdx.x / tiles_n;
+    if (chunk >= *a.plan.count) return;
+    TileRows rows;
+    const Tile tile = expert_tile(a, chunk, (int)blockIdx.x - chunk * tiles_n, rows);
+    if (tile.expert == a.E)
+        zero_tile(a, tile, rows, mm::BN);
+    else
+        matmul_body<WFMT, false, NARROW, 1, 4, true>(lds, a.w + (int64_t)tile.expert * a.stride, a.x, a.y, tile.count,
+                                                     a.N, a.nb, 1, rows);
+}
+
+template <int WFMT>
+static hipError_t launch_experts(const ExpertArgs &a, hipStream_t st) {
+    const bool narrow = tile_rows(a.pairs, a.E) == kNarrowRows;
+    int tiles_n = (a.N + mm::BN - 1) / mm::BN;
+    const int64_t grid = max_tiles(a.pairs, a.E, narrow ? kNarrowRows : kFullRows) * tiles_n;
+    ExpertArgs args = a;
+    void *argv[] = {(void *)&args, (void *)&tiles_n};
+    const void *k = narrow ? (const void *)k_experts_matmul<WFMT, true> : (const void *)k_experts_matmul<WFMT, false>;
+    return hipLaunchKernel(k, dim3((unsigned)grid), dim3(mm::NT), argv, 0, st);
+}
+
+hipError_t launch_experts_32(int fmt, const ExpertArgs &a, hipStream_t st) {
+    switch (fmt) {
+        case F_Q4_0: return launch_experts<F_Q4_0>(a, st);
+        case F_Q8_0: return launch_experts<F_Q8_0>(a, st);
+        case F_Q4_1: return launch_experts<F_Q4_1>(a, st);
+        case F_Q5_0: return launch_experts<F_Q5_0>(a, st);
+        case F_Q5_1: return launch_experts<F_Q5_1>(a, st);
+    }
+    return hipErrorInvalidValue;
 }
 
 // K = 32: one block per row, too short for the two-block stages above (the

@@ -49,7 +49,7 @@
 // the fold is acc += d8 * ((float)V * d - dmin * Mn).
 // Output lane layout of a 32x32 MFMA tile: lane l, register r holds row
 // 8(r/4) + 4(l/32) + r%4 and column l%32.
-#include "qmm_device.h"
+#include "moe.h"
 
 #include <type_traits>
 
@@ -172,9 +172,13 @@ __device__ __forceinline__ void q4k_sc_m(uint32_t s0, uint32_t s1, uint32_t s2, 
     }
 }
 
-template <int F, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4>
+// GROUPED: one tile of the experts' products.  M is its row count, w its
+// expert's matrix, `rows` says where its rows come from and go to.
+template <int F, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4, bool GROUPED = false>
 __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, const uint8_t *__restrict__ xq,
-                                              float *__restrict__ y, int M, int N, int ns, int tiles_m) {
+                                              float *__restrict__ y, int M, int N, int ns, int tiles_m,
+                                              const TileRows &rows = TileRows()) {
+    static_assert(!GROUPED || !SPLIT, "a tile of the experts' products has K whole");
     using namespace mk;
     using W = KW<F>;
     using KT = KN<F, G, WPG>;
@@ -199,7 +203,7 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
     constexpr int P = ksplit * G;
     const int tiles = (int)gridDim.x / ksplit;
     const int tile = (int)blockIdx.x % tiles, gpart = (int)blockIdx.x / tiles;
-    const int mt = tile % tiles_m, nt = tile / tiles_m;
+    const int mt = GROUPED ? 0 : tile % tiles_m, nt = GROUPED ? rows.nt : tile / tiles_m;
     const int m0 = mt * TBM, n0 = nt * BN;
     auto first_sb = [&](int p) { return (p * ns + P - 1) / P; };
     const int sh = (ns + 1) / 2;
@@ -221,9 +225,16 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
     // Rows past the matrix re-read its last row (their results are not
     // stored).
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(xq + (int64_t)m0 * xrow), 0, (int)((uint32_t)min(M - m0, TBM) * xrow), 0x00020000);
+        (void *)(xq + (int64_t)m0 * xrow), 0, (int)(GROUPED ? rows.x_bytes : (uint32_t)min(M - m0, TBM) * xrow),
+        0x00020000);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
         (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(N - n0, BN) * wrow), 0x00020000);
+    // the activation buffer's row of the tile's row
+    auto source = [&](int row) {
+        const int r = min(m0 + row, M - 1) - m0;
+        if constexpr (GROUPED) return (uint32_t)rows.src[r];
+        return (uint32_t)r;
+    };
     uint32_t voff[PER_WAVE];
 #pragma unroll
     for (int k = 0; k < PER_WAVE; ++k) {
@@ -233,7 +244,7 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
         } else if (q < XQN) {
             const int f0 = kWave * q + lane, f = NARROW ? min(f0, NBM * XC - 1) : f0;
             const int row = f / XC, c = f - XC * row;
-            voff[k] = (uint32_t)(min(m0 + row, M - 1) - m0) * xrow + (uint32_t)xchunk(c);
+            voff[k] = source(row) * xrow + (uint32_t)xchunk(c);
         } else {
             const int f = kWave * (q - XQN) + lane, row = f / WC, c = f - WC * row;
             voff[k] = (uint32_t)(min(n0 + row, N - 1) - n0) * wrow + (uint32_t)W::wchunk(c);
@@ -612,7 +623,9 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
                 const int m = m0 + 32 * TI * wm + 32 * i + 8 * (r >> 2) + 4 * lh + (r & 3);
                 if (m >= M) continue;
                 // two addends on a zeroed output: the same sum in either order
-                if constexpr (SPLIT)
+                if constexpr (GROUPED)
+                    y[(int64_t)rows.pair[m] * N + n] = acc[i][r];
+                else if constexpr (SPLIT)
                     atomicAdd(y + (int64_t)m * N + n, acc[i][r]);
                 else
                     y[(int64_t)m * N + n] = acc[i][r];
@@ -642,6 +655,47 @@ __global__ __launch_bounds__(64 * WPG * G) void k_matmul_k_narrow(const uint8_t 
                                                                   int M, int N, int ns, int tiles_m) {
     static_assert(mk::KN<F, G, WPG>::LDS_BYTES <= 160 * 1024, "LDS of one CU");
     matmul_k_body<F, SPLIT, true, G, WPG>(w, xq, y, M, N, ns, tiles_m);
+}
+
+// The experts' products: a tile of the plan and the weight rows of one workgroup
+// tile, consecutive workgroups on the same rows.
+template <int F, bool NARROW>
+__global__ __launch_bounds__(NARROW ? 256 : mk::NT) void k_experts_matmul_k(ExpertArgs a, int tiles_n) {
+    constexpr int BN = NARROW ? mk::KN<F, 1>::BN : mk::KW<F>::BN;
+    const int chunk = (int)blockIdx.x / tiles_n;
+    if (chunk >= *a.plan.count) return;
+    TileRows rows;
+    const Tile tile = expert_tile(a, chunk, (int)blockIdx.x - chunk * tiles_n, rows);
+    if (tile.expert == a.E)
+        zero_tile(a, tile, rows, BN);
+    else
+        matmul_k_body<F, false, NARROW, 1, 4, true>(a.w + (int64_t)tile.expert * a.stride, a.x, a.y, tile.count, a.N,
+                                                    a.nb, 1, rows);
+}
+
+template <int F>
+static hipError_t launch_experts(const ExpertArgs &a, hipStream_t st) {
+    const bool narrow = tile_rows(a.pairs, a.E) == kNarrowRows;
+    const int BN = narrow ? mk::KN<F, 1>::BN : mk::KW<F>::BN;
+    int tiles_n = (a.N + BN - 1) / BN;
+    const int64_t grid = max_tiles(a.pairs, a.E, narrow ? kNarrowRows : kFullRows) * tiles_n;
+    const void *k = narrow ? (const void *)k_experts_matmul_k<F, true> : (const void *)k_experts_matmul_k<F, false>;
+    const int lds = narrow ? mk::KN<F, 1>::LDS_BYTES : mk::KW<F>::LDS_BYTES;
+    static int lds_ok[2][kLdsDevices] = {};
+    const hipError_t e = allow_dynamic_lds(k, (size_t)lds, lds_ok[narrow]);
+    if (e != hipSuccess) return e;
+    ExpertArgs args = a;
+    void *argv[] = {(void *)&args, (void *)&tiles_n};
+    return hipLaunchKernel(k, dim3((unsigned)grid), dim3(narrow ? 256 : mk::NT), argv, (size_t)lds, st);
+}
+
+hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st) {
+    switch (fmt) {
+        case F_Q2_K: return launch_experts<F_Q2_K>(a, st);
+        case F_Q4_K: return launch_experts<F_Q4_K>(a, st);
+        case F_Q6_K: return launch_experts<F_Q6_K>(a, st);
+    }
+    return hipErrorInvalidValue;
 }
 
 // Largest super-block count whose tile offsets fit the 32-bit buffer offsets
