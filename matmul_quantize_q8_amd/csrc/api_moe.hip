@@ -21,6 +21,8 @@ hipError_t launch_experts_few_q5_1(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_few_q2_k(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_few_q4_k(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_few_q6_k(const ExpertArgs &a, hipStream_t st);
+hipError_t launch_experts_stream_32(int fmt, const ExpertArgs &a, hipStream_t st);
+hipError_t launch_experts_stream_k(int fmt, const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_32(int fmt, const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st);
 int64_t matmul_q4_0_max_blocks();
@@ -99,13 +101,17 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
     QMM_TRY(check_device());
     ExpertArgs a = {static_cast<const uint8_t *>(w), stride, static_cast<const uint8_t *>(xq),
                     (uint32_t)(x_rows * nb * xbytes), x_rows == pairs, y, nullptr, {}, (int)pairs, (int)top_k, (int)E,
-                    (int)N, (int)nb};
+                    (int)N, (int)nb, tile_rows(pairs, E)};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (pairs <= kSelfPairs)
         a.ids = ids;
     else
         a.plan = plan_at(plan, pairs, E);
-    if (pairs <= kSelfPairs || tile_rows(pairs, E) == kFewRows || nb < 2) return launched(few(a, st));
+    // one token's experts have a row each: the decode product's way
+    if (T == 1 || nb < 2) return launched(few(a, st));
+    // whole stages of 256 values
+    if (a.rows <= kNarrowRows && (k || nb % 8 == 0))
+        return launched(k ? launch_experts_stream_k(fmt, a, st) : launch_experts_stream_32(fmt, a, st));
     return launched(k ? launch_experts_k(fmt, a, st) : launch_experts_32(fmt, a, st));
 }
 

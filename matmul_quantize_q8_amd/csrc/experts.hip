@@ -15,10 +15,9 @@ constexpr int kPlanWaves = 16;
 
 struct PlanArgs {
     const int *ids;
-    int *count;
     Tile *tiles;
     int *pair, *token;
-    int pairs, top, E, rows, bits;
+    int pairs, top, E, rows, most, bits;        // most: tiles that there is room for
 };
 
 __device__ __forceinline__ uint64_t same_lanes(int key, int bits, bool live) {
@@ -32,9 +31,9 @@ __device__ __forceinline__ uint64_t same_lanes(int key, int bits, bool live) {
 }
 
 __global__ __launch_bounds__(64 * kPlanWaves) void k_experts_plan(PlanArgs a) {
-    extern __shared__ int plan_lds[];                     // [waves][E + 1] counts, then places; [E + 1] sums
+    extern __shared__ int plan_lds[];                     // [waves][E + 1] counts, then places; [E + 1] first rows; [waves]
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = a.E + 1;
-    int *counts = plan_lds, *mine = counts + wave * n, *total = counts + kPlanWaves * n, *scan = total + n;
+    int *counts = plan_lds, *mine = counts + wave * n, *first = counts + kPlanWaves * n, *scan = first + n;
     for (int i = threadIdx.x; i < kPlanWaves * n; i += 64 * kPlanWaves) counts[i] = 0;
     __syncthreads();
     const int each = ((a.pairs + 64 * kPlanWaves - 1) / (64 * kPlanWaves)) * 64;
@@ -49,8 +48,8 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_experts_plan(PlanArgs a) {
         if (p < hi && __builtin_ctzll(m) == lane) mine[key] += __popcll(m);
     }
     __syncthreads();
-    // thread e sums expert e (E + 1 of them fit the workgroup): places inside the expert for each wave, and two
-    // sums over the experts (rows before, tiles before) by doubling steps
+    // thread e sums expert e (E + 1 of them fit the workgroup): places inside the
+    // expert for each wave, and the tiles before it
     const int e = threadIdx.x;
     int rows = 0;
     if (e < n) {
@@ -61,33 +60,30 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_experts_plan(PlanArgs a) {
         }
     }
     const int tiles = (rows + a.rows - 1) / a.rows;
-    int before_rows = 0, before_tiles = 0;
-    {
-        // inclusive sums in each wave, then the waves' totals
-        int r = rows, t = tiles;
+    int upto = tiles;                                     // inclusive sum in the wave, then the waves before
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int pr = __shfl_up(r, d, kWave), pt = __shfl_up(t, d, kWave);
-            if (lane >= d) r += pr, t += pt;
-        }
-        if (lane == 63) scan[2 * wave] = r, scan[2 * wave + 1] = t;
-        __syncthreads();
-        for (int w = 0; w < wave; ++w) before_rows += scan[2 * w], before_tiles += scan[2 * w + 1];
-        before_rows += r - rows;
-        before_tiles += t - tiles;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d, kWave);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    int before = upto - tiles, all = 0;
+    for (int w = 0; w < kPlanWaves; ++w) {
+        if (w < wave) before += scan[w];
+        all += scan[w];
     }
     if (e < n) {
-        total[e] = before_rows;
-        for (int k = 0; k < tiles; ++k)
-            a.tiles[before_tiles + k] = {e, before_rows + k * a.rows, min(a.rows, rows - k * a.rows), 0};
-        if (e == n - 1) *a.count = before_tiles + tiles;
+        first[e] = before * a.rows;
+        for (int k = 0; k < tiles; ++k) a.tiles[before + k] = {e, min(a.rows, rows - k * a.rows)};
     }
+    for (int k = all + threadIdx.x; k < a.most; k += 64 * kPlanWaves) a.tiles[k] = {0, 0};
     __syncthreads();
     for (int p = lo + lane; p - lane < hi; p += 64) {
         const int key = key_of(p);
         const uint64_t m = same_lanes(key, a.bits, p < hi);
         if (p < hi) {
-            const int at = total[key] + mine[key] + __popcll(m & ((1ull << lane) - 1));
+            const int at = first[key] + mine[key] + __popcll(m & ((1ull << lane) - 1));
             a.pair[at] = p;
             a.token[at] = p / a.top;
         }
@@ -100,9 +96,10 @@ static_assert(kMaxExperts + 1 <= 64 * kPlanWaves, "a thread for every expert");
 hipError_t launch_experts_plan(const int *ids, void *plan, int pairs, int top, int E, hipStream_t st) {
     if (pairs <= kSelfPairs) return hipSuccess;
     const Plan p = plan_at(plan, pairs, E);
-    PlanArgs a = {ids, const_cast<int *>(p.count), const_cast<Tile *>(p.tiles), const_cast<int *>(p.pair),
-                  const_cast<int *>(p.token), pairs, top, E, tile_rows(pairs, E), 32 - __builtin_clz((unsigned)E)};
-    const size_t lds = (size_t)((kPlanWaves + 1) * (E + 1) + 2 * kPlanWaves) * 4;      // 35 KB at most
+    const int rows = tile_rows(pairs, E);
+    PlanArgs a = {ids, const_cast<Tile *>(p.tiles), const_cast<int *>(p.pair), const_cast<int *>(p.token), pairs, top, E,
+                  rows, (int)max_tiles(pairs, E, rows), 32 - __builtin_clz((unsigned)E)};
+    const size_t lds = (size_t)((kPlanWaves + 1) * (E + 1) + kPlanWaves) * 4;      // 35 KB at most
     void *args[] = {(void *)&a};
     return hipLaunchKernel((const void *)k_experts_plan, dim3(1), dim3(64 * kPlanWaves), args, lds, st);
 }

@@ -1,0 +1,204 @@
+// Experts' products of up to 32 rows a tile on MFMA: what the 32-value formats
+// (experts_stream_32.hip) and the K-quants (experts_stream_k.hip) share.
+//
+// Bound by the weight stream: with a few rows a tile every weight byte is used for
+// little work, so what counts is how many bytes are on their way.
+//   * A stage is 256 values of every row: a weight row's part (84 bytes of Q2_K ..
+//     272 of Q8_0) is copied in 16-byte chunks, consecutive lanes on consecutive
+//     chunks, and one barrier, one wait and one chain of LDS reads serve all of it.
+//     Stages of two blocks, as the prefill tiles of the 32-value formats have them,
+//     leave a workgroup that is nearly alone on its compute unit waiting for that
+//     chain (1.8 TB/s of Q8_0 weights, whatever the depth of its ring).
+//   * A wave copies its own 32 weight rows into one LDS buffer, empties it into
+//     registers at the start of a step and at once copies the next stage into it:
+//     a stage is on its way during all of a step, at half the LDS of two buffers,
+//     and three or four workgroups share a compute unit (128 experts of
+//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 27.7 us, 64 tokens 54.7 ->
+//     47.7; Q8_0, 64 tokens 117 -> 77).  Only the activations, which the waves
+//     share, have two buffers.
+//   * Tiles of 16 rows where an expert has few: less LDS, less of the fold.
+//
+// A workgroup: a tile's rows x 32 WPG weight rows, wave w of a group alone on weight
+// rows 32 w .., one 32 x 32 MFMA tile a step of K; G groups of WPG waves, each on
+// its part of K, which join in LDS in a fixed order.
+#pragma once
+
+#include <type_traits>
+#include <utility>
+
+#include "moe.h"
+
+namespace qmm {
+
+namespace es {
+constexpr float kBias = 12582912.0f;               // 1.5 * 2^23, bit pattern 0x4B400000
+
+// LDS of a K group of WPG waves, for an activation row of XC chunks and a weight row
+// of WC chunks a stage; XD bytes of a wave's own.
+template <int ROWS, int WPG, int XC, int WC, int XD> struct Layout {
+    static constexpr int WL = (32 * WC + kWave - 1) / kWave;  // wave loads of a wave's 32 weight rows
+    static constexpr int XL = (ROWS * XC + kWave - 1) / kWave, NA = (XL + WPG - 1) / WPG;    // of the activations; of those a wave's
+    static constexpr int XAREA = XL * 1024, WAREA = WL * 1024;
+    static constexpr int WAT = 2 * XAREA, DXAT = WAT + WPG * WAREA, OWN = XD, LDS = DXAT + WPG * XD;
+};
+}  // namespace es
+
+// 16 bytes a lane from a buffer into LDS at m0base + 16 * lane; inline assembly, so
+// that the compiler does not wait for the copies in flight before each LDS read.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void stream_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t m0base, uint32_t voff, int soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(m0base), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// The loop over the stages of one tile.  C: the format's constants and its step,
+//   C::XBYTES, WBYTES    bytes of a stage of an activation and of a weight row
+//   C::xchunk, wchunk    where chunk c of them starts
+//   C::Step              empty() takes the weights out of LDS, work() uses them
+template <class C, int ROWS, int FR, int G, int WPG>
+__device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &a, const uint8_t *w, int M,
+                                            const TileRows &rows) {
+    using namespace es;
+    using L = typename C::template Lds<ROWS, WPG>;
+    constexpr int BN = 32 * WPG;                           // weight rows of the workgroup
+    const int lane = threadIdx.x & 63, wave = uniform((threadIdx.x >> 6) % WPG);
+    const int grp = G == 1 ? 0 : uniform((threadIdx.x >> 6) / WPG);
+    uint8_t *const lds = lds_all + grp * L::LDS;
+    const int lr = lane & 31;
+    const int n0 = rows.nt * BN, all = a.nb / C::BLOCKS;              // stages of a row; this group's are [s0, s1)
+    const int s0 = all * grp / G, s1 = all * (grp + 1) / G;
+    const int steps = (all + G - 1) / G;                   // every wave passes the same barriers
+    const uint32_t wrow = (uint32_t)all * C::WBYTES, xrow = (uint32_t)all * C::XBYTES;
+    const __amdgpu_buffer_rsrc_t xr =
+        __builtin_amdgcn_make_buffer_rsrc((void *)a.x, 0, (int)rows.x_bytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(a.N - n0, BN) * wrow), 0x00020000);
+    // copies: rows past the matrix, and past the tile, repeat its last
+    uint32_t xoff[L::NA], woff[L::WL], xat[L::NA];
+#pragma unroll
+    for (int k = 0; k < L::NA; ++k) {
+        const int q = min(wave + WPG * k, L::XL - 1), f = min(kWave * q + lane, ROWS * C::XC - 1), row = f / C::XC;
+        xoff[k] = (uint32_t)rows.src[min(row, M - 1)] * xrow + (uint32_t)C::xchunk(f - C::XC * row);
+        xat[k] = 1024u * (uint32_t)q;
+    }
+#pragma unroll
+    for (int k = 0; k < L::WL; ++k) {
+        const int f = min(kWave * k + lane, 32 * C::WC - 1), row = f / C::WC;
+        woff[k] = (uint32_t)(min(n0 + 32 * wave + row, a.N - 1) - n0) * wrow + (uint32_t)C::wchunk(f - C::WC * row);
+    }
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
+    const uint32_t w0 = (uint32_t)uniform((int)(lds0 + L::WAT + L::WAREA * wave));
+    auto copy_weights = [&](int s) {
+#pragma unroll
+        for (int k = 0; k < L::WL; ++k) stream_to_lds(wr, w0 + 1024 * k, woff[k], s * C::WBYTES);
+    };
+    auto copy_rows = [&](int s, int buffer) {
+#pragma unroll
+        for (int k = 0; k < L::NA; ++k)
+            stream_to_lds(xr, (uint32_t)uniform((int)(lds0 + buffer * L::XAREA + xat[k])), xoff[k], s * C::XBYTES);
+    };
+    typename C::template Step<ROWS, FR> step(lds + L::WAT + L::WAREA * wave + 16 * C::WC * lr,
+                                             lds + L::DXAT + L::OWN * wave, lane);
+    if (s0 < s1) {
+        copy_weights(s0);
+        copy_rows(s0, 0);
+    }
+    // A step waits for its own copies of the stage, the barrier publishes every
+    // wave's activations (and tells that the buffer of the stage before is free).
+    for (int i = 0; i < steps; ++i) {
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const int s = s0 + i;
+        if (G > 1 && s >= s1) continue;                    // another group has one stage more
+        if (s + 1 < s1) copy_rows(s + 1, (i + 1) & 1);
+        step.empty();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // the weights are in registers
+        if (s + 1 < s1) copy_weights(s + 1);
+        step.work(lds + (i & 1) * L::XAREA);
+    }
+    if constexpr (G > 1) {
+        // the other groups hand their sums to group 0 through LDS, which adds them in
+        // the groups' order
+        static_assert((G - 1) * WPG * 4096 <= G * L::LDS, "the sums fit");
+        float *sums = reinterpret_cast<float *>(lds_all) + 1024 * wave + lane;
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (grp > 0) {
+#pragma unroll
+            for (int r = 0; r < 4 * FR; ++r) sums[1024 * WPG * (grp - 1) + 64 * r] = step.acc[r];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (grp > 0) return;
+#pragma unroll
+        for (int g = 1; g < G; ++g)
+#pragma unroll
+            for (int r = 0; r < 4 * FR; ++r) step.acc[r] += sums[1024 * WPG * (g - 1) + 64 * r];
+    }
+    const int n = n0 + 32 * wave + lr;                     // lane l, register r: row 8 (r / 4) + 4 (l / 32) + r % 4
+    if (n >= a.N) return;
+#pragma unroll
+    for (int r = 0; r < 4 * FR; ++r) {
+        const int m = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (m < M) a.y[(int64_t)rows.pair[m] * a.N + n] = step.acc[r] * C::OUT_SCALE;
+    }
+}
+
+template <class C, int ROWS, int G, int WPG>
+__global__ __launch_bounds__(64 * G * WPG) void k_experts_stream(ExpertArgs a, int tiles_n) {
+    using L = typename C::template Lds<ROWS, WPG>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t stream_lds[];
+    int *pair = reinterpret_cast<int *>(stream_lds + G * L::LDS), *src = pair + ROWS;
+    const int chunk = (int)blockIdx.x / tiles_n;
+    const Tile tile = expert_tile(a, chunk, pair, src);
+    if (tile.count == 0) return;
+    __syncthreads();
+    const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};
+    if (tile.expert == a.E) {
+        zero_tile(a, tile.count, rows, 32 * WPG);
+        return;
+    }
+    const uint8_t *w = a.w + (int64_t)tile.expert * a.stride;
+    if (tile.count <= 8)
+        stream_tile<C, ROWS, 1, G, WPG>(stream_lds, a, w, tile.count, rows);
+    else if (ROWS == 16 || tile.count <= 16)
+        stream_tile<C, ROWS, 2, G, WPG>(stream_lds, a, w, tile.count, rows);
+    else
+        stream_tile<C, ROWS, ROWS / 8, G, WPG>(stream_lds, a, w, tile.count, rows);
+}
+
+template <class C, int ROWS, int G, int WPG>
+static hipError_t launch_stream(const ExpertArgs &a, hipStream_t st) {
+    constexpr int lds = G * C::template Lds<ROWS, WPG>::LDS + 8 * ROWS;
+    static_assert(lds <= kMaxLdsBytes, "LDS of one CU");
+    const void *k = (const void *)k_experts_stream<C, ROWS, G, WPG>;
+    static int lds_ok[kLdsDevices] = {};
+    const hipError_t e = allow_dynamic_lds(k, (size_t)lds, lds_ok);
+    if (e != hipSuccess) return e;
+    int tiles_n = (a.N + 32 * WPG - 1) / (32 * WPG);
+    ExpertArgs args = a;
+    void *argv[] = {(void *)&args, (void *)&tiles_n};
+    return hipLaunchKernel(k, dim3((unsigned)(grid_tiles(a) * tiles_n)), dim3(64 * G * WPG), argv, (size_t)lds, st);
+}
+
+template <class C, int ROWS>
+static hipError_t pick_stream(const ExpertArgs &a, hipStream_t st) {
+    // Blocks of 128 weight rows that the call is likely to have, every expert in use,
+    // and the workgroup that suits them (us, Q4_0 weights, one group of four waves /
+    // two of two / four of two):   40 blocks, 4 experts of 512 x 2048  17.1 / 10.8 / 8.9
+    //   114, 16 of 768 x 2048  11.3 / 9.0 / 8.5       128, 64 of 1024 x 2048  9.8 / 7.6 / 7.6
+    //   336, 8 of 3584 x 4096  33.0 / 24.8 / 29.3     448, 8 of 3500 x 4096  43.0 / 42.3 / 44.4
+    //   over 1000, 128 of 1536 x 2048  26.2 / 27.2 / 41.8 (16 tokens)  44.4 / 47.4 / 67.8 (64)
+    const int64_t tiles = (a.pairs < a.E ? a.pairs : a.E) + a.pairs / a.rows;
+    const int64_t blocks = tiles * ((a.N + 127) / 128);
+    if (blocks >= 3 * kCUs / 2) return launch_stream<C, ROWS, 1, 4>(a, st);
+    if (blocks >= kCUs / 2) return launch_stream<C, ROWS, 2, 2>(a, st);
+    return launch_stream<C, ROWS, 4, 2>(a, st);
+}
+
+template <class C>
+static hipError_t experts_stream(const ExpertArgs &a, hipStream_t st) {
+    if (a.rows > kNarrowRows) return hipErrorInvalidValue;             // the kernel's tables
+    return a.rows <= kFewRows ? pick_stream<C, kFewRows>(a, st) : pick_stream<C, kNarrowRows>(a, st);
+}
+
+}  // namespace qmm

@@ -187,7 +187,8 @@ __device__ __forceinline__ void each_index(std::integer_sequence<int, I...>, Fn 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // GROUPED: one tile of the experts' products.  M is its row count, w its
 // expert's matrix, `rows` says where its rows come from and go to.
-template <int WFMT, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4, bool GROUPED = false>
+// FR: the rows (8 FR of the narrow tile's 32) that the fold works out.
+template <int WFMT, bool SPLIT, bool NARROW = false, int G = 1, int WPG = 4, bool GROUPED = false, int FR = 4>
 __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restrict__ w,
                                             const uint8_t *__restrict__ xq, float *__restrict__ y, int M, int N,
                                             int nb, int tiles_m, const TileRows &rows = TileRows()) {
@@ -252,9 +253,8 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
         (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(N - n0, TBN) * wrow), 0x00020000);
     // the activation buffer's row of the tile's row
     auto source = [&](int row) {
-        const int r = min(m0 + row, M - 1) - m0;
-        if constexpr (GROUPED) return (uint32_t)rows.src[r];
-        return (uint32_t)r;
+        if constexpr (GROUPED) return (uint32_t)rows.src[min(row, M - 1)];
+        return (uint32_t)(min(m0 + row, M - 1) - m0);
     };
     uint32_t voff[PER_WAVE];
     uint32_t m0k[PER_WAVE];   // narrow: the LDS base of each of this wave's loads
@@ -410,7 +410,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
     auto load_dx = [&](int kb, int i, float (&d)[16]) {
         const float4 *p = reinterpret_cast<const float4 *>(lds + dxw + 4 * (64 * kb + 32 * i + 4 * lh));
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
+        for (int a = 0; a < FR; ++a) {
             const float4 q = p[2 * a];
             d[4 * a] = q.x;
             d[4 * a + 1] = q.y;
@@ -424,7 +424,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
     auto fold = [&](const v16i &d, int i, int j, const float (&dx)[16], float dw, float nbias) {
         float u[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < 4 * FR; ++r) {
             // element first, then reinterpret: __builtin_bit_cast applied
             // directly to a vector element reads element 0 with this
             // toolchain (hipcc 7.2), so it must not be used here
@@ -433,7 +433,7 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(u[r], dx[r], acc[i][j][r]);
+        for (int r = 0; r < 4 * FR; ++r) acc[i][j][r] = fmaf(u[r], dx[r], acc[i][j][r]);
     };
 
     // Chunks of one stage for this lane: per A tile the block-0 and block-1
@@ -699,6 +699,9 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
         }
     };
 
+    // the upper half of a tile of at most 64 rows: this wave only copies
+    const bool idle = GROUPED && !NARROW && 64 * wm >= M;
+
     // Stage s lives in buffer s % NB.  At step s this wave's loads of stage
     // s have landed once at most the PER_WAVE loads of each later stage in
     // flight are outstanding; the barrier publishes every wave's and frees
@@ -711,7 +714,10 @@ __device__ __forceinline__ void matmul_body(uint8_t *lds, const uint8_t *__restr
         constexpr int b = decltype(bc)::value;
         asm volatile("s_waitcnt vmcnt(%0)" :: "i"((NB - 2) * PER_WAVE) : "memory");
         lds_barrier();
-        if (G == 1 || s < nst) compute(ldsg + b * STAGE, 2 * s + 1 == nbp, min(s + NB - 1, nst - 1), (b + NB - 1) % NB);
+        if (GROUPED && idle)
+            dma(min(s + NB - 1, nst - 1), (b + NB - 1) % NB);
+        else if (G == 1 || s < nst)
+            compute(ldsg + b * STAGE, 2 * s + 1 == nbp, min(s + NB - 1, nst - 1), (b + NB - 1) % NB);
     };
 #pragma unroll
     for (int k = 0; k + 1 < NB; ++k) dma(min(k, nst - 1), k);
@@ -877,27 +883,42 @@ __global__ __launch_bounds__(mm::NT, 2) void k_matmul_narrow(const uint8_t *__re
 }
 
 // The experts' products: a tile of the plan and 128 weight rows of its expert to
-// a workgroup, consecutive workgroups on the same rows.
+// a workgroup, consecutive workgroups on the same rows.  Tiles of up to 32 rows come
+// here only where rows are no whole stages of 256 values.
 template <int WFMT, bool NARROW>
 __global__ __launch_bounds__(mm::NT, 2) void k_experts_matmul(ExpertArgs a, int tiles_n) {
     constexpr int LDS = NARROW ? mm::WN<WFMT>::template LDS_BYTES<1> : mm::WF<WFMT>::LDS_BYTES;
+    constexpr int MOST = NARROW ? kNarrowRows : kFullRows;
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+    __shared__ int pair[MOST], src[MOST];
     const int chunk = (int)blockIdx.x / tiles_n;
-    if (chunk >= *a.plan.count) return;
-    TileRows rows;
-    const Tile tile = expert_tile(a, chunk, (int)blockIdx.x - chunk * tiles_n, rows);
-    if (tile.expert == a.E)
-        zero_tile(a, tile, rows, mm::BN);
-    else
-        matmul_body<WFMT, false, NARROW, 1, 4, true>(lds, a.w + (int64_t)tile.expert * a.stride, a.x, a.y, tile.count,
-                                                     a.N, a.nb, 1, rows);
+    const Tile tile = expert_tile(a, chunk, pair, src);
+    if (tile.count == 0) return;
+    __syncthreads();
+    const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};
+    if (tile.expert == a.E) {
+        zero_tile(a, tile.count, rows, mm::BN);
+        return;
+    }
+    const uint8_t *w = a.w + (int64_t)tile.expert * a.stride;
+    if constexpr (NARROW) {
+        if (tile.count <= 8)
+            matmul_body<WFMT, false, true, 1, 4, true, 1>(lds, w, a.x, a.y, tile.count, a.N, a.nb, 1, rows);
+        else if (tile.count <= 16)
+            matmul_body<WFMT, false, true, 1, 4, true, 2>(lds, w, a.x, a.y, tile.count, a.N, a.nb, 1, rows);
+        else
+            matmul_body<WFMT, false, true, 1, 4, true, 4>(lds, w, a.x, a.y, tile.count, a.N, a.nb, 1, rows);
+    } else {
+        matmul_body<WFMT, false, false, 1, 4, true>(lds, w, a.x, a.y, tile.count, a.N, a.nb, 1, rows);
+    }
 }
 
 template <int WFMT>
 static hipError_t launch_experts(const ExpertArgs &a, hipStream_t st) {
-    const bool narrow = tile_rows(a.pairs, a.E) == kNarrowRows;
+    const bool narrow = a.rows <= kNarrowRows;
+    if (a.rows > kFullRows) return hipErrorInvalidValue;          // the kernel's tables
     int tiles_n = (a.N + mm::BN - 1) / mm::BN;
-    const int64_t grid = max_tiles(a.pairs, a.E, narrow ? kNarrowRows : kFullRows) * tiles_n;
+    const int64_t grid = grid_tiles(a) * tiles_n;
     ExpertArgs args = a;
     void *argv[] = {(void *)&args, (void *)&tiles_n};
     const void *k = narrow ? (const void *)k_experts_matmul<WFMT, true> : (const void *)k_experts_matmul<WFMT, false>;

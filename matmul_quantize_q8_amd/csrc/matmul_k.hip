@@ -231,9 +231,8 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
         (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(N - n0, BN) * wrow), 0x00020000);
     // the activation buffer's row of the tile's row
     auto source = [&](int row) {
-        const int r = min(m0 + row, M - 1) - m0;
-        if constexpr (GROUPED) return (uint32_t)rows.src[r];
-        return (uint32_t)r;
+        if constexpr (GROUPED) return (uint32_t)rows.src[min(row, M - 1)];
+        return (uint32_t)(min(m0 + row, M - 1) - m0);
     };
     uint32_t voff[PER_WAVE];
 #pragma unroll
@@ -328,7 +327,8 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
 
     // One stage: the wave's B tile (32 weight rows) against all four A tiles
     // (128 tokens), so that each B operand is built once per workgroup.
-    auto compute = [&](const uint8_t *sb) __attribute__((always_inline)) {
+    auto compute_tiles = [&](const uint8_t *sb, auto ni) __attribute__((always_inline)) {
+        constexpr int TI = decltype(ni)::value;
         if constexpr (F == F_Q2_K) {
             store_d8(sb);
             // the B tile's 16 scale bytes and d, dmin
@@ -575,6 +575,21 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
         }
     };
 
+    // A tiles that hold rows of the matrix: a tile of the experts' products may end
+    // in the middle of a wave's, or before it.
+    const int live = GROUPED ? uniform(min(max((M - 32 * TI * wm + 31) / 32, 0), TI)) : TI;
+    auto compute = [&](const uint8_t *sb) __attribute__((always_inline)) {
+        if (live == TI) {
+            compute_tiles(sb, std::integral_constant<int, TI>());
+        } else if constexpr (GROUPED) {
+            if (live == 1) compute_tiles(sb, std::integral_constant<int, 1>());
+            if constexpr (TI == 4) {
+                if (live == 2) compute_tiles(sb, std::integral_constant<int, 2>());
+                if (live == 3) compute_tiles(sb, std::integral_constant<int, 3>());
+            }
+        }
+    };
+
     // Super-block s0 + j lives in buffer j % 2.  At step j: wait for this
     // wave's loads of it, the barrier publishes every wave's (and tells that
     // the previous one's buffer is free), the DMA of the next goes into it,
@@ -657,36 +672,38 @@ __global__ __launch_bounds__(64 * WPG * G) void k_matmul_k_narrow(const uint8_t 
     matmul_k_body<F, SPLIT, true, G, WPG>(w, xq, y, M, N, ns, tiles_m);
 }
 
-// The experts' products: a tile of the plan and the weight rows of one workgroup
-// tile, consecutive workgroups on the same rows.
-template <int F, bool NARROW>
-__global__ __launch_bounds__(NARROW ? 256 : mk::NT) void k_experts_matmul_k(ExpertArgs a, int tiles_n) {
-    constexpr int BN = NARROW ? mk::KN<F, 1>::BN : mk::KW<F>::BN;
+// The experts' products of many rows: a tile of the plan and the weight rows of one
+// workgroup tile, consecutive workgroups on the same rows.
+template <int F>
+__global__ __launch_bounds__(mk::NT) void k_experts_matmul_k(ExpertArgs a, int tiles_n) {
+    constexpr int BN = mk::KW<F>::BN;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    int *pair = reinterpret_cast<int *>(lds + mk::KW<F>::LDS_BYTES), *src = pair + kFullRows;
     const int chunk = (int)blockIdx.x / tiles_n;
-    if (chunk >= *a.plan.count) return;
-    TileRows rows;
-    const Tile tile = expert_tile(a, chunk, (int)blockIdx.x - chunk * tiles_n, rows);
+    const Tile tile = expert_tile(a, chunk, pair, src);
+    if (tile.count == 0) return;
+    __syncthreads();
+    const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};
     if (tile.expert == a.E)
-        zero_tile(a, tile, rows, BN);
+        zero_tile(a, tile.count, rows, BN);
     else
-        matmul_k_body<F, false, NARROW, 1, 4, true>(a.w + (int64_t)tile.expert * a.stride, a.x, a.y, tile.count, a.N,
-                                                    a.nb, 1, rows);
+        matmul_k_body<F, false, false, 1, 4, true>(a.w + (int64_t)tile.expert * a.stride, a.x, a.y, tile.count, a.N,
+                                                   a.nb, 1, rows);
 }
 
 template <int F>
 static hipError_t launch_experts(const ExpertArgs &a, hipStream_t st) {
-    const bool narrow = tile_rows(a.pairs, a.E) == kNarrowRows;
-    const int BN = narrow ? mk::KN<F, 1>::BN : mk::KW<F>::BN;
+    if (a.rows > kFullRows) return hipErrorInvalidValue;          // the kernel's tables
+    constexpr int BN = mk::KW<F>::BN, lds = mk::KW<F>::LDS_BYTES + 8 * kFullRows;
+    static_assert(lds <= kMaxLdsBytes, "LDS of one CU");
     int tiles_n = (a.N + BN - 1) / BN;
-    const int64_t grid = max_tiles(a.pairs, a.E, narrow ? kNarrowRows : kFullRows) * tiles_n;
-    const void *k = narrow ? (const void *)k_experts_matmul_k<F, true> : (const void *)k_experts_matmul_k<F, false>;
-    const int lds = narrow ? mk::KN<F, 1>::LDS_BYTES : mk::KW<F>::LDS_BYTES;
-    static int lds_ok[2][kLdsDevices] = {};
-    const hipError_t e = allow_dynamic_lds(k, (size_t)lds, lds_ok[narrow]);
+    const void *k = (const void *)k_experts_matmul_k<F>;
+    static int lds_ok[kLdsDevices] = {};
+    const hipError_t e = allow_dynamic_lds(k, (size_t)lds, lds_ok);
     if (e != hipSuccess) return e;
     ExpertArgs args = a;
     void *argv[] = {(void *)&args, (void *)&tiles_n};
-    return hipLaunchKernel(k, dim3((unsigned)grid), dim3(narrow ? 256 : mk::NT), argv, (size_t)lds, st);
+    return hipLaunchKernel(k, dim3((unsigned)(grid_tiles(a) * tiles_n)), dim3(mk::NT), argv, (size_t)lds, st);
 }
 
 hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st) {

@@ -14,12 +14,19 @@ constexpr int64_t kMaxPairs = int64_t(1) << 26;
 // every workgroup of the product finds its rows from the ids by itself.
 constexpr int64_t kSelfPairs = kWave;
 
-// Rows of a tile: what one workgroup of a product takes of an expert's rows.
-constexpr int kFewRows = 8, kNarrowRows = 32, kFullRows = 128;
+// Rows of a tile: what one workgroup of a product takes of an expert's rows.  Short
+// tiles stream the weights (experts_stream.h), tiles of 128 rows are the prefill
+// matmul's.  Rows an expert, where they meet (us, 16 / 32 / 128 rows, 1536 x 2048):
+// 128 experts, 8 a token, Q4_0: 8 rows 54 / 56 / 147, 16 rows 68 / 69 / 147, 32 rows
+// 103 / 97 / 160, 64 rows 169 / 159 / 172, 128 rows - / 269 / 238; Q8_0: 64 rows 247 /
+// 209 / 184, 128 rows - / 345 / 255; Q4_K: 64 rows - / 125 / 153, 128 rows - / 211 / 226.
+// A few thousand pairs make too few workgroups of 128 rows (8 experts of 1024 x 1024,
+// 1400 pairs: 14.7 us in tiles of 32, 22 of 128).
+constexpr int kFewRows = 16, kNarrowRows = 32, kFullRows = 128;
 
 inline int tile_rows(int64_t pairs, int64_t experts) {
     const int64_t each = pairs / experts;
-    return each < 8 ? kFewRows : each < 64 ? kNarrowRows : kFullRows;
+    return each < 24 ? kFewRows : each < 96 || pairs < 4096 ? kNarrowRows : kFullRows;
 }
 
 // Most tiles that `pairs` rows in experts + 1 groups (the last: pairs without
@@ -31,27 +38,27 @@ inline int64_t max_tiles(int64_t pairs, int64_t experts, int rows) {
 
 struct Tile {
     int expert;                 // E: pairs without an expert, whose rows are zeros
-    int start, count;           // its pairs: order[start .. start + count)
-    int unused;
+    int count;                  // its rows; 0: no tile
 };
 
-// The plan in memory: [1 int: number of tiles, padded to 16 bytes][tiles][pairs
-// sorted by expert][their tokens].
+// The plan in memory: [most tiles][most tiles * rows pairs][their tokens].  A tile's
+// rows are at its own place, so a workgroup loads them beside the tile.
 struct Plan {
-    const int *count;
     const Tile *tiles;
     const int *pair, *token;
 };
 
 inline int64_t plan_bytes(int64_t pairs, int64_t experts) {
-    return 16 + 16 * max_tiles(pairs, experts, tile_rows(pairs, experts)) + 8 * pairs;
+    const int rows = tile_rows(pairs, experts);
+    return max_tiles(pairs, experts, rows) * (8 + 8 * rows);
 }
 
 inline Plan plan_at(const void *plan, int64_t pairs, int64_t experts) {
-    const char *p = static_cast<const char *>(plan);
-    const int64_t tiles = 16 * max_tiles(pairs, experts, tile_rows(pairs, experts));
-    const int *order = reinterpret_cast<const int *>(p + 16 + tiles);
-    return {reinterpret_cast<const int *>(p), reinterpret_cast<const Tile *>(p + 16), order, order + pairs};
+    const int rows = tile_rows(pairs, experts);
+    const int64_t tiles = max_tiles(pairs, experts, rows);
+    const Tile *t = static_cast<const Tile *>(plan);
+    const int *pair = reinterpret_cast<const int *>(t + tiles);
+    return {t, pair, pair + tiles * rows};
 }
 
 // A product over experts.
@@ -65,6 +72,7 @@ struct ExpertArgs {
     const int *ids;             // [pairs]; with it instead of the plan: kSelfPairs at most
     Plan plan;
     int pairs, top, E, N, nb;   // nb: blocks of a row
+    int rows;                   // rows of a tile
 };
 
 // s = round(x + residual), xq = Q8(y), y = s (offset + weight) / sqrt(mean(s^2) + eps).
@@ -102,28 +110,58 @@ struct RouteArgs {
 
 // The rows of one tile, for the matrix-instruction kernels.
 struct TileRows {
-    const int *pair, *src;      // output rows and activation rows of the tile's rows
+    const int *pair, *src;      // output rows and activation rows of the tile's rows (LDS)
     uint32_t x_bytes;
     int nt;                     // which columns of the output
 };
 
-// Tile `chunk` of the plan and where its rows are.
-__device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int nt, TileRows &rows) {
-    Tile t = a.plan.tiles[chunk];
-    t.expert = uniform(t.expert);
-    t.start = uniform(t.start);
-    t.count = uniform(t.count);
-    rows = {a.plan.pair + t.start, (a.x_per_pair ? a.plan.pair : a.plan.token) + t.start, a.x_bytes, nt};
+// Tile `chunk` of a product and its rows, into LDS tables of at least a.rows
+// entries: of the plan, or in a call without one the pairs of pair `chunk`'s
+// expert, if it is the first of every a.rows of them (count 0 otherwise).  The
+// caller has a barrier before the tables are read.
+__device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int *pair, int *src) {
+    Tile t;
+    const int most = a.rows;
+    if (a.ids != nullptr) {
+        const int lane = threadIdx.x & 63, id = lane < a.pairs ? a.ids[lane] : -1;
+        const int e = __builtin_amdgcn_readlane(id, chunk);
+        const bool none = (unsigned)e >= (unsigned)a.E;
+        uint64_t m = none ? 1ull << chunk : __ballot(lane < a.pairs && id == e);
+        const int before = __popcll(m & ((1ull << chunk) - 1));
+        if (before % most) return {0, 0};
+        m &= ~0ull << chunk;
+        t = {none ? a.E : e, min((int)__popcll(m), most)};
+        if (threadIdx.x < kWave && (m >> lane) & 1) {
+            const int r = __popcll(m & ((1ull << lane) - 1));
+            if (r < most) pair[r] = lane, src[r] = a.x_per_pair ? lane : lane / a.top;
+        }
+    } else {
+        // loaded beside the tile: rows past its count are whatever the plan holds
+        int p = 0, x = 0;
+        if ((int)threadIdx.x < most) {
+            p = a.plan.pair[(int64_t)chunk * most + threadIdx.x];
+            x = a.x_per_pair ? p : a.plan.token[(int64_t)chunk * most + threadIdx.x];
+        }
+        t = a.plan.tiles[chunk];
+        t.expert = uniform(t.expert);
+        t.count = uniform(t.count);
+        if ((int)threadIdx.x < t.count) pair[threadIdx.x] = p, src[threadIdx.x] = x;
+    }
     return t;
 }
 
 // Zeros in the workgroup's columns of pairs without an expert.
-__device__ __forceinline__ void zero_tile(const ExpertArgs &a, const Tile &t, const TileRows &rows, int columns) {
+__device__ __forceinline__ void zero_tile(const ExpertArgs &a, int count, const TileRows &rows, int columns) {
     const int n0 = rows.nt * columns, n = min(columns, a.N - n0);
-    for (int i = threadIdx.x; i < t.count * n; i += blockDim.x) {
+    for (int i = threadIdx.x; i < count * n; i += blockDim.x) {
         const int r = i / n;
         a.y[(int64_t)rows.pair[r] * a.N + n0 + (i - r * n)] = 0.0f;
     }
+}
+
+// Tiles that a product's grid holds for its calls with and without a plan.
+inline int64_t grid_tiles(const ExpertArgs &a) {
+    return a.ids != nullptr ? a.pairs : max_tiles(a.pairs, a.E, a.rows);
 }
 
 }  // namespace qmm

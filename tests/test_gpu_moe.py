@@ -344,7 +344,24 @@ def test_experts_planned(env, fmt, T, top, E, N, blocks, per_pair):
     _product(env, fmt, T, top, E, N, K, per_pair, _ids(np.random.default_rng(T), T, top, E, skew=True))
 
 
-@pytest.mark.parametrize("T", [9, 40, 300, 1500])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,top,E,N,K,per_pair", [
+    (40, 2, 64, 768, 512, False), (200, 2, 16, 1800, 256, True),         # many workgroups: 16 and 32 rows a tile
+    (20, 4, 16, 896, 1280, False), (100, 2, 8, 1400, 768, True),         # a few hundred
+    (2100, 2, 8, 136, 512, False), (1030, 4, 5, 300, 256, True)])        # 128 rows a tile
+def test_experts_large(env, fmt, T, top, E, N, K, per_pair):
+    torch, q, orc = env
+    _say("experts large", fmt, T, top, E, N, K, per_pair)
+    _product(env, fmt, T, top, E, N, K, per_pair, _ids(np.random.default_rng(T), T, top, E, skew=T < 1000))
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0", "q4_1", "q5_0", "q5_1"])
+def test_experts_128_rows_of_odd_blocks(env, fmt):
+    _say("experts odd blocks", fmt)
+    _product(env, fmt, 2100, 2, 8, 24, 288, False, _ids(np.random.default_rng(3), 2100, 2, 8))
+
+
+@pytest.mark.parametrize("T", [9, 40, 300, 1500, 2500])
 @pytest.mark.parametrize("fmt", ["q4_0", "q4_k"])
 def test_experts_unusual_ids(env, fmt, T):
     """Ids outside the experts give zeros; one expert for all; the same expert twice for a token; experts unused."""
