@@ -72,7 +72,7 @@ qmm_status glu(int fmt, const void *gate, const void *up, void *xq, int dtype, i
     QMM_TRY(check_in(up, dtype, rows, F, us));
     QMM_TRY(check_ptrs({xq}));
     QMM_TRY(check_device());
-    const GluArgs a = {gate, up, static_cast<uint8_t *>(xq), rows, gs, us, (int)(F / 4)};
+    const GluArgs a = {gate, up, static_cast<uint8_t *>(xq), rows, gs, us, (int)(F / row_values(dtype))};
     return launched(launch_glu(dtype, fmt, act, a, static_cast<hipStream_t>(stream)));
 }
 
@@ -151,7 +151,7 @@ qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *
     QMM_TRY(check_device());
     const bool grouped = groups > 1 && groups_kept < groups;            // all groups kept: none are left out
     const RouteArgs a = {logits, bias, ids, weights, T, logits_stride, (int)E, (int)top_k, grouped ? (int)groups : 1,
-                         (int)groups_kept, (int)group_top, score == QMM_SCORE_SOFTMAX, renorm != 0, scale};
+                         (int)groups_kept, (int)group_top, score == QMM_SCORE_SOFTMAX, renorm != 0, scale, 0};
     return launched(launch_route(dtype, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -7,18 +7,36 @@ namespace qmm {
 // ---------------------------------------------------------------------------
 // Plan: a stable counting sort of the pairs by expert (an id outside [0, E)
 // counts as expert E, whose rows the products fill with zeros), and the tiles.
-// One workgroup; wave w takes the w-th stretch of the pairs, 64 at a time.  The
-// lanes that hold the same expert find one another by a ballot for each bit of
-// its number, so no atomic is needed and the order is that of the pairs.
+// A workgroup takes a segment of the pairs, wave w of it the w-th stretch, 64 at a
+// time.  The lanes that hold the same expert find one another by a ballot for each
+// bit of its number, so no atomic orders anything and the order is that of the pairs.
+// More than one segment: a launch before it counts each segment's pairs, and every
+// workgroup sums those of the segments before its own.  Bound by latency; one workgroup
+// for all pairs would be bound by its compute unit's vector units (32768 pairs of 64
+// experts: 48 us in one workgroup, 8.8 in 32 after a count).
 // ---------------------------------------------------------------------------
 constexpr int kPlanWaves = 16;
 
 struct PlanArgs {
     const int *ids;
     Tile *tiles;
-    int *pair, *token;
+    int *pair, *token, *counts;                 // counts: [segments][E + 1]
     int pairs, top, E, rows, most, bits;        // most: tiles that there is room for
+    int segment, segments;
 };
+
+__global__ __launch_bounds__(256) void k_experts_count(PlanArgs a) {
+    extern __shared__ int count_lds[];
+    const int n = a.E + 1, lo = blockIdx.x * a.segment, hi = min(lo + a.segment, a.pairs);
+    for (int i = threadIdx.x; i < n; i += 256) count_lds[i] = 0;
+    __syncthreads();
+    for (int p = lo + threadIdx.x; p < hi; p += 256) {
+        const int id = a.ids[p];
+        atomicAdd(count_lds + ((unsigned)id < (unsigned)a.E ? id : a.E), 1);    // a sum of whole numbers: any order
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256) a.counts[(int64_t)blockIdx.x * n + i] = count_lds[i];
+}
 
 __device__ __forceinline__ uint64_t same_lanes(int key, int bits, bool live) {
     uint64_t m = __ballot(live);
@@ -30,34 +48,65 @@ __device__ __forceinline__ uint64_t same_lanes(int key, int bits, bool live) {
     return m;
 }
 
+// HOLD ids a lane; longer segments (HOLD < 0) come in batches of -HOLD, twice.
+template <int HOLD>
 __global__ __launch_bounds__(64 * kPlanWaves) void k_experts_plan(PlanArgs a) {
+    constexpr int N = HOLD < 0 ? -HOLD : HOLD;
     extern __shared__ int plan_lds[];                     // [waves][E + 1] counts, then places; [E + 1] first rows; [waves]
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = a.E + 1;
-    int *counts = plan_lds, *mine = counts + wave * n, *first = counts + kPlanWaves * n, *scan = first + n;
-    for (int i = threadIdx.x; i < kPlanWaves * n; i += 64 * kPlanWaves) counts[i] = 0;
-    __syncthreads();
-    const int each = ((a.pairs + 64 * kPlanWaves - 1) / (64 * kPlanWaves)) * 64;
-    const int lo = min(wave * each, a.pairs), hi = min(lo + each, a.pairs);
-    auto key_of = [&](int p) {
-        const int id = p < hi ? a.ids[p] : 0;
-        return (unsigned)id < (unsigned)a.E ? id : a.E;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6, n = a.E + 1;
+    int *counts = plan_lds, *mine = counts + wave * n, *first = counts + waves * n, *scan = first + n;
+    const int from0 = blockIdx.x * a.segment, end = min(from0 + a.segment, a.pairs);
+    const int each = (a.segment + 64 * waves - 1) / (64 * waves) * 64;
+    const int lo = min(from0 + wave * each, end), hi = min(lo + each, end);
+    int key[N];
+    auto load = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = from + 64 * i + lane;
+            key[i] = p < hi ? a.ids[p] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = (unsigned)key[i] < (unsigned)a.E ? key[i] : a.E;
     };
-    for (int p = lo + lane; p - lane < hi; p += 64) {
-        const int key = key_of(p);
-        const uint64_t m = same_lanes(key, a.bits, p < hi);
-        if (p < hi && __builtin_ctzll(m) == lane) mine[key] += __popcll(m);
-    }
+    load(lo);
+    for (int i = threadIdx.x; i < waves * n; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    // fn(key, pair, lanes with the same key) of every 64 pairs of the wave, in order
+    auto walk = [&](auto fn) {
+        for (int from = lo; from < hi; from += 64 * N) {
+            if (HOLD < 0) load(from);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int p = from + 64 * i + lane;
+                if (p - lane >= hi) break;
+                fn(key[i], p, same_lanes(key[i], a.bits, p < hi));
+            }
+        }
+    };
+    walk([&](int k, int p, uint64_t m) {
+        if (p < hi && __builtin_ctzll(m) == lane) mine[k] += __popcll(m);
+    });
     __syncthreads();
     // thread e sums expert e (E + 1 of them fit the workgroup): places inside the
-    // expert for each wave, and the tiles before it
+    // expert for each wave, after the segments before this one, and the tiles before it
     const int e = threadIdx.x;
     int rows = 0;
     if (e < n) {
-        for (int w = 0; w < kPlanWaves; ++w) {
-            const int c = counts[w * n + e];
-            counts[w * n + e] = rows;
-            rows += c;
+        int place = 0;
+        if (a.segments > 1) {
+#pragma unroll 8
+            for (int s = 0; s < a.segments; ++s) {
+                const int c = a.counts[(int64_t)s * n + e];
+                rows += c;
+                place += s < (int)blockIdx.x ? c : 0;
+            }
         }
+        for (int w = 0; w < waves; ++w) {
+            const int c = counts[w * n + e];
+            counts[w * n + e] = place;
+            place += c;
+        }
+        if (a.segments == 1) rows = place;
     }
     const int tiles = (rows + a.rows - 1) / a.rows;
     int upto = tiles;                                     // inclusive sum in the wave, then the waves before
@@ -69,26 +118,26 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_experts_plan(PlanArgs a) {
     if (lane == 63) scan[wave] = upto;
     __syncthreads();
     int before = upto - tiles, all = 0;
-    for (int w = 0; w < kPlanWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
         if (w < wave) before += scan[w];
         all += scan[w];
     }
     if (e < n) {
         first[e] = before * a.rows;
-        for (int k = 0; k < tiles; ++k) a.tiles[before + k] = {e, min(a.rows, rows - k * a.rows)};
+        // each workgroup writes some of the tiles
+        for (int k = blockIdx.x; k < tiles; k += gridDim.x) a.tiles[before + k] = {e, min(a.rows, rows - k * a.rows)};
     }
-    for (int k = all + threadIdx.x; k < a.most; k += 64 * kPlanWaves) a.tiles[k] = {0, 0};
+    if (blockIdx.x == 0)
+        for (int k = all + threadIdx.x; k < a.most; k += blockDim.x) a.tiles[k] = {0, 0};
     __syncthreads();
-    for (int p = lo + lane; p - lane < hi; p += 64) {
-        const int key = key_of(p);
-        const uint64_t m = same_lanes(key, a.bits, p < hi);
+    walk([&](int k, int p, uint64_t m) {
         if (p < hi) {
-            const int at = first[key] + mine[key] + __popcll(m & ((1ull << lane) - 1));
+            const int at = first[k] + mine[k] + __popcll(m & ((1ull << lane) - 1));
             a.pair[at] = p;
             a.token[at] = p / a.top;
         }
-        if (p < hi && __builtin_ctzll(m) == lane) mine[key] += __popcll(m);
-    }
+        if (p < hi && __builtin_ctzll(m) == lane) mine[k] += __popcll(m);
+    });
 }
 
 static_assert(kMaxExperts + 1 <= 64 * kPlanWaves, "a thread for every expert");
@@ -97,11 +146,24 @@ hipError_t launch_experts_plan(const int *ids, void *plan, int pairs, int top, i
     if (pairs <= kSelfPairs) return hipSuccess;
     const Plan p = plan_at(plan, pairs, E);
     const int rows = tile_rows(pairs, E);
-    PlanArgs a = {ids, const_cast<Tile *>(p.tiles), const_cast<int *>(p.pair), const_cast<int *>(p.token), pairs, top, E,
-                  rows, (int)max_tiles(pairs, E, rows), 32 - __builtin_clz((unsigned)E)};
-    const size_t lds = (size_t)((kPlanWaves + 1) * (E + 1) + kPlanWaves) * 4;      // 35 KB at most
+    PlanArgs a = {ids, const_cast<Tile *>(p.tiles), const_cast<int *>(p.pair), const_cast<int *>(p.token),
+                  const_cast<int *>(p.counts), pairs, top, E, rows, (int)max_tiles(pairs, E, rows),
+                  32 - __builtin_clz((unsigned)E), (int)plan_segment(pairs), (int)plan_segments(pairs)};
     void *args[] = {(void *)&a};
-    return hipLaunchKernel((const void *)k_experts_plan, dim3(1), dim3(64 * kPlanWaves), args, lds, st);
+    if (a.segments > 1) {
+        const hipError_t e = hipLaunchKernel((const void *)k_experts_count, dim3((unsigned)a.segments), dim3(256), args,
+                                             (size_t)(E + 1) * 4, st);
+        if (e != hipSuccess) return e;
+    }
+    // a wave for every 64 pairs and for every 64 experts, 16 at most
+    const int want = (a.segment + 63) / 64, least = (E + 64) / 64;
+    const int waves = want < least ? least : want < kPlanWaves ? want : kPlanWaves;
+    const size_t lds = (size_t)((waves + 1) * (E + 1) + waves) * 4;           // 35 KB at most
+    const int each = (want + waves - 1) / waves;
+    const void *k = each <= 1   ? (const void *)k_experts_plan<1>
+                    : each <= 2 ? (const void *)k_experts_plan<2>
+                                : (const void *)k_experts_plan<-16>;
+    return hipLaunchKernel(k, dim3((unsigned)a.segments), dim3((unsigned)(64 * waves)), args, lds, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -20,18 +20,21 @@ constexpr int64_t kGluGrid = 1 << 22;          // workgroups of a launch: a grid
 
 template <int RT, int FMT, int ACT>
 __global__ __launch_bounds__(kGluThreads) void k_glu(GluArgs a) {
-    const int64_t row_bytes = (int64_t)(a.quads / (act_values(FMT) / 4)) * act_bytes(FMT);
-    const int64_t all = a.rows * a.quads;
+    constexpr int V = row_values(RT);                     // 16 bytes a lane
+    const int64_t row_bytes = (int64_t)(a.pieces / (act_values(FMT) / V)) * act_bytes(FMT);
+    const int64_t all = a.rows * a.pieces;
     for (int64_t base = (int64_t)blockIdx.x * kGluThreads; base < all; base += (int64_t)gridDim.x * kGluThreads) {
-        const int64_t row0 = base / a.quads;
-        const uint32_t at = (uint32_t)(base - row0 * a.quads) + threadIdx.x;
-        const int64_t row = row0 + at / (uint32_t)a.quads;
-        const int c = (int)(at % (uint32_t)a.quads);
+        const int64_t row0 = base / a.pieces;
+        const uint32_t at = (uint32_t)(base - row0 * a.pieces) + threadIdx.x;
+        const int64_t row = row0 + at / (uint32_t)a.pieces;
+        const int c = (int)(at % (uint32_t)a.pieces);
         if (row >= a.rows) continue;
-        const float4 g = load4<RT>(a.gate, row * a.gs + 4 * c), u = load4<RT>(a.up, row * a.us + 4 * c);
-        store_quantized<FMT>(a.xq + row * row_bytes, c,
-                             make_float4(activation<ACT>(g.x) * u.x, activation<ACT>(g.y) * u.y,
-                                         activation<ACT>(g.z) * u.z, activation<ACT>(g.w) * u.w));
+        float g[V], u[V];
+        load_row<RT, V>(a.gate, row * a.gs + V * c, g);
+        load_row<RT, V>(a.up, row * a.us + V * c, u);
+#pragma unroll
+        for (int k = 0; k < V; ++k) g[k] = activation<ACT>(g[k]) * u[k];
+        store_quantized<FMT, V>(a.xq + row * row_bytes, c, g);
     }
 }
 
@@ -40,7 +43,7 @@ static hipError_t launch(int act, GluArgs a, hipStream_t st) {
     const void *k = act == G_SILU   ? (const void *)k_glu<RT, FMT, G_SILU>
                     : act == G_GELU ? (const void *)k_glu<RT, FMT, G_GELU>
                                     : (const void *)k_glu<RT, FMT, G_GELU_TANH>;
-    const int64_t grid = (a.rows * a.quads + kGluThreads - 1) / kGluThreads;
+    const int64_t grid = (a.rows * a.pieces + kGluThreads - 1) / kGluThreads;
     void *args[] = {(void *)&a};
     return hipLaunchKernel(k, dim3((unsigned)(grid < kGluGrid ? grid : kGluGrid)), dim3(kGluThreads), args, 0, st);
 }

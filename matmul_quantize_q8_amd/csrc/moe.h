@@ -41,16 +41,30 @@ struct Tile {
     int count;                  // its rows; 0: no tile
 };
 
-// The plan in memory: [most tiles][most tiles * rows pairs][their tokens].  A tile's
-// rows are at its own place, so a workgroup loads them beside the tile.
+// Pairs that one workgroup of the plan sorts: all of them up to 2048, then 1024, or
+// so many that there are at most 256 such segments.
+inline int64_t plan_segment(int64_t pairs) {
+    if (pairs <= 2048) return pairs;
+    const int64_t s = (pairs + 255) / 256;
+    return s <= 1024 ? 1024 : (s + 63) / 64 * 64;
+}
+inline int64_t plan_segments(int64_t pairs) {
+    const int64_t s = plan_segment(pairs);
+    return (pairs + s - 1) / s;
+}
+
+// The plan in memory: [most tiles][most tiles * rows pairs][their tokens][segments][E + 1
+// pairs of each expert, where there are several segments].  A tile's rows are at its
+// own place, so a workgroup loads them beside the tile.
 struct Plan {
     const Tile *tiles;
-    const int *pair, *token;
+    const int *pair, *token, *counts;
 };
 
 inline int64_t plan_bytes(int64_t pairs, int64_t experts) {
     const int rows = tile_rows(pairs, experts);
-    return max_tiles(pairs, experts, rows) * (8 + 8 * rows);
+    const int64_t segments = plan_segments(pairs);
+    return max_tiles(pairs, experts, rows) * (8 + 8 * rows) + (segments > 1 ? segments * (experts + 1) * 4 : 0);
 }
 
 inline Plan plan_at(const void *plan, int64_t pairs, int64_t experts) {
@@ -58,7 +72,7 @@ inline Plan plan_at(const void *plan, int64_t pairs, int64_t experts) {
     const int64_t tiles = max_tiles(pairs, experts, rows);
     const Tile *t = static_cast<const Tile *>(plan);
     const int *pair = reinterpret_cast<const int *>(t + tiles);
-    return {t, pair, pair + tiles * rows};
+    return {t, pair, pair + tiles * rows, pair + 2 * tiles * rows};
 }
 
 // A product over experts.
@@ -93,7 +107,7 @@ struct GluArgs {
     const void *gate, *up;
     uint8_t *xq;
     int64_t rows, gs, us;       // strides in elements
-    int quads;                  // F / 4
+    int pieces;                 // of a row, 16 bytes each
 };
 
 // A token's top experts and their weights.
@@ -106,6 +120,7 @@ struct RouteArgs {
     int E, top, groups, kept, group_top;
     int softmax, renorm;
     float scale;
+    int group_bits;             // set by the launch
 };
 
 // The rows of one tile, for the matrix-instruction kernels.
