@@ -574,7 +574,7 @@ qmm_status qmm_experts_plan(const int32_t *ids, void *plan, int64_t plan_bytes, 
  *   xq   : x_rows rows of Q8_0 (K-quants: Q8_K) blocks, less than 4 GiB.
  *   ids, plan, plan_bytes : the ids that the plan was made of, and the plan.
  *   y    : f32 [T * top_k][N], written.
- * N <= 2^20, T * top_k * N <= 2^36, K as for qmm_matmul_*. */
+ * N <= 2^18, T * top_k * N <= 2^35, K as for qmm_matmul_*. */
 qmm_status qmm_experts_matmul_q4_0(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,
                                    const int32_t *ids, const void *plan, int64_t plan_bytes, float *y, int64_t T,
                                    int64_t top_k, int64_t E, int64_t N, int64_t K, void *stream);
@@ -605,7 +605,7 @@ qmm_status qmm_experts_matmul_q6_k(const void *w, int64_t expert_stride, const v
  *   y        : f32 [T * top_k][N], 16-byte aligned.    weights : f32 [T][top_k].
  *   residual : rows [T][N], or NULL.
  *   out      : rows [T][N], written.  May be residual itself.
- * N <= 2^20, T * top_k * N <= 2^36.  Where N is no multiple of 4, rows may have any
+ * N <= 2^18, T * top_k * N <= 2^35.  Where N is no multiple of 4, rows may have any
  * alignment and stride. */
 qmm_status qmm_experts_combine(const float *y, const float *weights, const void *residual, void *out, int dtype,
                                int64_t T, int64_t top_k, int64_t N, int64_t residual_stride, int64_t out_stride,

@@ -22,6 +22,7 @@ hipError_t launch_experts_few_q2_k(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_few_q4_k(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_few_q6_k(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_stream_32(int fmt, const ExpertArgs &a, hipStream_t st);
+bool experts_stream_32_suits(int fmt, const ExpertArgs &a);
 hipError_t launch_experts_stream_k(int fmt, const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_32(int fmt, const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st);
@@ -33,8 +34,8 @@ namespace {
 
 using namespace qmm;
 
-constexpr int64_t kMaxOutputs = int64_t(1) << 36;      // values of a product
-constexpr int64_t kMaxRows = int64_t(1) << 20;         // weight rows of an expert
+constexpr int64_t kMaxOutputs = int64_t(1) << 35;      // values of a product: its grid holds less than 2^32 threads
+constexpr int64_t kMaxRows = int64_t(1) << 18;         // weight rows of an expert
 
 bool act_shape_ok(int fmt, int64_t T, int64_t K) {
     if (T < 1 || T > kMaxDim || K < act_values(fmt) || K > kMaxDim || K % act_values(fmt) != 0) return false;
@@ -107,10 +108,10 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
         a.ids = ids;
     else
         a.plan = plan_at(plan, pairs, E);
-    // one token's experts have a row each: the decode product's way
-    if (T == 1 || nb < 2) return launched(few(a, st));
-    // whole stages of 256 values
-    if (a.rows <= kNarrowRows && (k || nb % 8 == 0))
+    // one token's experts have a row each: the decode product's way; a single block of 32
+    // values is no stage of any other
+    if (T == 1 || (!k && nb < 2)) return launched(few(a, st));
+    if (a.rows <= kNarrowRows && (k || experts_stream_32_suits(fmt, a)))
         return launched(k ? launch_experts_stream_k(fmt, a, st) : launch_experts_stream_32(fmt, a, st));
     return launched(k ? launch_experts_k(fmt, a, st) : launch_experts_32(fmt, a, st));
 }

@@ -14,6 +14,7 @@
 namespace qmm {
 
 constexpr int kFewWaves = 4;
+constexpr int kFewTiles = 32768;                       // of a launch: they lie along the grid's y, which holds 65535
 
 template <int BIT>
 __device__ __forceinline__ float sum_below(float v) {
@@ -22,7 +23,7 @@ __device__ __forceinline__ float sum_below(float v) {
 }
 
 template <int F, bool PAIRED, int LPR, int RI>
-__global__ __launch_bounds__(64 * kFewWaves) void k_experts_few(ExpertArgs a, int xs, int ss) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_experts_few(ExpertArgs a, int tile0, int xs, int ss) {
     using FB = FmtBytes<F>;
     using UT = ::qmm::Unit<F, PAIRED>;
     extern __shared__ uint4 lds_dyn[];
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_few(ExpertArgs a, in
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t row0 = ((int64_t)blockIdx.x * kFewWaves + wave) * RW;
     const int nrows = (int)max((int64_t)0, min((int64_t)RW, (int64_t)a.N - row0));
-    const Tile tile = expert_tile(a, blockIdx.y, pairs, sources);
+    const Tile tile = expert_tile(a, tile0 + (int)blockIdx.y, pairs, sources);
     if (tile.count == 0) return;
     __syncthreads();
     if (tile.expert == a.E) {                          // no expert: zeros
@@ -110,8 +111,14 @@ static hipError_t launch_few(const ExpertArgs &a, hipStream_t st) {
     if (e != hipSuccess) return e;
     const int row_blocks = (a.N + RW * kFewWaves - 1) / (RW * kFewWaves);
     ExpertArgs args = a;
-    void *argv[] = {(void *)&args, (void *)&xs, (void *)&ss};
-    return hipLaunchKernel(k, dim3((unsigned)row_blocks, (unsigned)grid_tiles(a)), dim3(64 * kFewWaves), argv, lds, st);
+    const int tiles = (int)grid_tiles(a);
+    for (int tile0 = 0; tile0 < tiles; tile0 += kFewTiles) {
+        void *argv[] = {(void *)&args, (void *)&tile0, (void *)&xs, (void *)&ss};
+        const int y = tiles - tile0 < kFewTiles ? tiles - tile0 : kFewTiles;
+        const hipError_t le = hipLaunchKernel(k, dim3((unsigned)row_blocks, (unsigned)y), dim3(64 * kFewWaves), argv, lds, st);
+        if (le != hipSuccess) return le;
+    }
+    return hipSuccess;
 }
 
 template <int F, bool PAIRED>

@@ -55,8 +55,17 @@ __device__ __forceinline__ void stream_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t
 
 // The loop over the stages of one tile.  C: the format's constants and its step,
 //   C::XBYTES, WBYTES    bytes of a stage of an activation and of a weight row
-//   C::xchunk, wchunk    where chunk c of them starts
+//   C::XC, WC            chunks of them in LDS;  xchunk, wchunk: where chunk c starts
 //   C::Step              empty() takes the weights out of LDS, work() uses them
+//
+// A row that is no whole number of stages (TAIL) ends with a stage of its last BLOCKS
+// blocks, of which work() skips those that the stage before had.
+//
+// C::WLEAD, XLEAD, parts of 2 mod 4 bytes: every other one, along a row or down the rows,
+// starts two bytes off the dword grid, where a copy takes four times as long (27 ns a wave
+// against 7).  Such a part is copied from two bytes before and its LDS row starts with
+// this lead; the chunk that brings the part's end (of Q6_K the last, of the others one
+// more, MORE) is moved by two bytes, so that it too starts on the grid.
 template <class C, int ROWS, int FR, int G, int WPG>
 __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &a, const uint8_t *w, int M,
                                             const TileRows &rows) {
@@ -67,40 +76,67 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
     const int grp = G == 1 ? 0 : uniform((threadIdx.x >> 6) / WPG);
     uint8_t *const lds = lds_all + grp * L::LDS;
     const int lr = lane & 31;
-    const int n0 = rows.nt * BN, all = a.nb / C::BLOCKS;              // stages of a row; this group's are [s0, s1)
+    const int n0 = rows.nt * BN, all = (a.nb + C::BLOCKS - 1) / C::BLOCKS;     // stages of a row; this group's are [s0, s1)
     const int s0 = all * grp / G, s1 = all * (grp + 1) / G;
     const int steps = (all + G - 1) / G;                   // every wave passes the same barriers
-    const uint32_t wrow = (uint32_t)all * C::WBYTES, xrow = (uint32_t)all * C::XBYTES;
-    const __amdgpu_buffer_rsrc_t xr =
-        __builtin_amdgcn_make_buffer_rsrc((void *)a.x, 0, (int)rows.x_bytes, 0x00020000);
+    constexpr int WB = C::WBYTES / C::BLOCKS, XB = C::XBYTES / C::BLOCKS;
+    const uint32_t wrow = (uint32_t)a.nb * WB, xrow = (uint32_t)a.nb * XB;
+    // up to two bytes past the last row, in its last dword
+    const uint32_t x_bytes = C::XLEAD ? (rows.x_bytes + 3) & ~3u : rows.x_bytes;
+    const uint32_t w_bytes = (uint32_t)min(a.N - n0, BN) * wrow;
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void *)a.x, 0, (int)x_bytes, 0x00020000);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(w + (int64_t)n0 * wrow), 0, (int)((uint32_t)min(a.N - n0, BN) * wrow), 0x00020000);
+        (void *)(w + (int64_t)n0 * wrow), 0, (int)(C::WLEAD ? (w_bytes + 3) & ~3u : w_bytes), 0x00020000);
     // copies: rows past the matrix, and past the tile, repeat its last
     uint32_t xoff[L::NA], woff[L::WL], xat[L::NA];
+    // what a stage that starts at an odd block adds: its scalar offset is two bytes less
+    int xstep[C::XLEAD ? L::NA : 1], wstep[C::WLEAD ? L::WL : 1];
 #pragma unroll
     for (int k = 0; k < L::NA; ++k) {
         const int q = min(wave + WPG * k, L::XL - 1), f = min(kWave * q + lane, ROWS * C::XC - 1), row = f / C::XC;
-        xoff[k] = (uint32_t)rows.src[min(row, M - 1)] * xrow + (uint32_t)C::xchunk(f - C::XC * row);
+        const int c = f - C::XC * row;
+        const uint32_t r = (uint32_t)rows.src[min(row, M - 1)];
+        xoff[k] = r * xrow + (uint32_t)C::xchunk(c);
         xat[k] = 1024u * (uint32_t)q;
+        if constexpr (C::XLEAD) {
+            const bool off = r & a.nb & 1, more = c >= C::MORE * C::XBYTES / 16;
+            xoff[k] += off ? (more ? 2 : -2) : 0;
+            xstep[k] = off == more ? 0 : 4;
+        }
     }
 #pragma unroll
     for (int k = 0; k < L::WL; ++k) {
-        const int f = min(kWave * k + lane, 32 * C::WC - 1), row = f / C::WC;
-        woff[k] = (uint32_t)(min(n0 + 32 * wave + row, a.N - 1) - n0) * wrow + (uint32_t)C::wchunk(f - C::WC * row);
+        const int f = min(kWave * k + lane, 32 * C::WC - 1), row = f / C::WC, c = f - C::WC * row;
+        const int r = min(n0 + 32 * wave + row, a.N - 1);
+        woff[k] = (uint32_t)(r - n0) * wrow + (uint32_t)C::wchunk(c);
+        if constexpr (C::WLEAD) {
+            const bool off = r & a.nb & 1, more = c >= C::MORE * C::WBYTES / 16;
+            woff[k] += off ? (more ? 2 : -2) : 0;
+            wstep[k] = off == more ? 0 : 4;
+        }
     }
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
     const uint32_t w0 = (uint32_t)uniform((int)(lds0 + L::WAT + L::WAREA * wave));
+    // the stage's first block
+    auto first = [&](int s) { return C::TAIL ? min(s * C::BLOCKS, a.nb - C::BLOCKS) : s * C::BLOCKS; };
     auto copy_weights = [&](int s) {
+        const int at = first(s);
 #pragma unroll
-        for (int k = 0; k < L::WL; ++k) stream_to_lds(wr, w0 + 1024 * k, woff[k], s * C::WBYTES);
+        for (int k = 0; k < L::WL; ++k)
+            stream_to_lds(wr, w0 + 1024 * k, C::WLEAD && (at & 1) ? woff[k] + wstep[C::WLEAD ? k : 0] : woff[k],
+                          C::WLEAD ? at * WB & ~3 : at * WB);
     };
     auto copy_rows = [&](int s, int buffer) {
+        const int at = first(s);
 #pragma unroll
         for (int k = 0; k < L::NA; ++k)
-            stream_to_lds(xr, (uint32_t)uniform((int)(lds0 + buffer * L::XAREA + xat[k])), xoff[k], s * C::XBYTES);
+            stream_to_lds(xr, (uint32_t)uniform((int)(lds0 + buffer * L::XAREA + xat[k])),
+                          C::XLEAD && (at & 1) ? xoff[k] + xstep[C::XLEAD ? k : 0] : xoff[k],
+                          C::XLEAD ? at * XB & ~3 : at * XB);
     };
     typename C::template Step<ROWS, FR> step(lds + L::WAT + L::WAREA * wave + 16 * C::WC * lr,
                                              lds + L::DXAT + L::OWN * wave, lane);
+    if constexpr (C::XLEAD || C::WLEAD) step.parities(min(n0 + 32 * wave + lr, a.N - 1) & a.nb, rows.src, M);
     if (s0 < s1) {
         copy_weights(s0);
         copy_rows(s0, 0);
@@ -112,10 +148,10 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
         const int s = s0 + i;
         if (G > 1 && s >= s1) continue;                    // another group has one stage more
         if (s + 1 < s1) copy_rows(s + 1, (i + 1) & 1);
-        step.empty();
+        step.empty(first(s));
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // the weights are in registers
         if (s + 1 < s1) copy_weights(s + 1);
-        step.work(lds + (i & 1) * L::XAREA);
+        step.work(lds + (i & 1) * L::XAREA, first(s), s * C::BLOCKS - first(s));
     }
     if constexpr (G > 1) {
         // the other groups hand their sums to group 0 through LDS, which adds them in
@@ -180,18 +216,23 @@ static hipError_t launch_stream(const ExpertArgs &a, hipStream_t st) {
     return hipLaunchKernel(k, dim3((unsigned)(grid_tiles(a) * tiles_n)), dim3(64 * G * WPG), argv, (size_t)lds, st);
 }
 
+// Blocks of 128 weight rows that the call is likely to have, every expert in use.
+constexpr int64_t kEnoughBlocks = 3 * kCUs / 2, kFewBlocks = kCUs / 2;       // for one group of waves each; for no two
+inline int64_t stream_blocks(const ExpertArgs &a) {
+    const int64_t tiles = (a.pairs < a.E ? a.pairs : a.E) + a.pairs / a.rows;
+    return tiles * ((a.N + 127) / 128);
+}
+
 template <class C, int ROWS>
 static hipError_t pick_stream(const ExpertArgs &a, hipStream_t st) {
-    // Blocks of 128 weight rows that the call is likely to have, every expert in use,
-    // and the workgroup that suits them (us, Q4_0 weights, one group of four waves /
-    // two of two / four of two):   40 blocks, 4 experts of 512 x 2048  17.1 / 10.8 / 8.9
+    // The workgroup that suits the call's blocks (us, Q4_0 weights, one group of four
+    // waves / two of two / four of two):   40 blocks, 4 experts of 512 x 2048  17.1 / 10.8 / 8.9
     //   114, 16 of 768 x 2048  11.3 / 9.0 / 8.5       128, 64 of 1024 x 2048  9.8 / 7.6 / 7.6
     //   336, 8 of 3584 x 4096  33.0 / 24.8 / 29.3     448, 8 of 3500 x 4096  43.0 / 42.3 / 44.4
     //   over 1000, 128 of 1536 x 2048  26.2 / 27.2 / 41.8 (16 tokens)  44.4 / 47.4 / 67.8 (64)
-    const int64_t tiles = (a.pairs < a.E ? a.pairs : a.E) + a.pairs / a.rows;
-    const int64_t blocks = tiles * ((a.N + 127) / 128);
-    if (blocks >= 3 * kCUs / 2) return launch_stream<C, ROWS, 1, 4>(a, st);
-    if (blocks >= kCUs / 2) return launch_stream<C, ROWS, 2, 2>(a, st);
+    const int64_t blocks = stream_blocks(a);
+    if (blocks >= kEnoughBlocks) return launch_stream<C, ROWS, 1, 4>(a, st);
+    if (blocks >= kFewBlocks) return launch_stream<C, ROWS, 2, 2>(a, st);
     return launch_stream<C, ROWS, 4, 2>(a, st);
 }
 

@@ -20,13 +20,16 @@ template <int F>
 struct SuperBlocks {
     static constexpr int WBYTES = F == F_Q2_K ? kQ2KBytes : F == F_Q4_K ? kQ4KBytes : kQ6KBytes;
     static constexpr int BLOCKS = 1, XBYTES = kQ8KBytes;
+    static constexpr bool TAIL = false, XLEAD = false, WLEAD = F == F_Q6_K;         // the others' bytes are whole dwords
+    static constexpr int MORE = 2;                            // no chunk after a part's last
     // activation row: the codes in 16 chunks, the block sums in two, the chunk that starts with d
     static constexpr int XC = 19;
     static constexpr int xchunk(int c) { return c < 16 ? 4 + 16 * c : c == 16 ? 260 : c == 17 ? 276 : 0; }
     // weight row: chunks in order, the last one moved back to end with the super-block; an odd count, so that rows
     // start in many banks
     static constexpr int FULL = WBYTES / 16, WC = F == F_Q2_K ? 7 : F == F_Q4_K ? 9 : 15;
-    static constexpr int wchunk(int c) { return c < FULL ? 16 * c : WBYTES - 16; }
+    // (Q6_K's with a lead: the dword that holds its last two bytes is then at byte 16 FULL + 12)
+    static constexpr int wchunk(int c) { return c < FULL ? 16 * c : WLEAD ? (WBYTES + 3) / 4 * 4 - 16 : WBYTES - 16; }
     static constexpr float OUT_SCALE = 1.0f;
     // a wave's f32 d8 of a stage's rows
     template <int ROWS, int WPG> using Lds = es::Layout<ROWS, WPG, XC, WC, 4 * ROWS>;
@@ -36,7 +39,7 @@ struct SuperBlocks {
     struct Step {
         const uint8_t *ws;                                 // the lane's weight row
         float *d8w;
-        int lane, lh;
+        int lane, lh, wodd = 0;                            // wodd: Q6_K, of the weight row's first super-block
         v16i bias;
         // scales (with d and dmin), then the code bytes that the lane's half feeds
         static constexpr int NV = F == F_Q2_K ? 13 : F == F_Q4_K ? 20 : 29;
@@ -51,22 +54,33 @@ struct SuperBlocks {
         static __device__ __forceinline__ uint4 rd16(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
         static __device__ __forceinline__ float half_lo(uint32_t x) { return f16_bits_to_f32(x); }
 
-        __device__ __forceinline__ void empty() {
+        __device__ __forceinline__ void parities(int n, const int *, int) { wodd = n & 1; }
+        // eight bytes at byte o of a super-block behind its lead
+        __device__ __forceinline__ uint2 rd8(int o, uint32_t lead) const {
+            const uint2 q = *reinterpret_cast<const uint2 *>(ws + o);
+            const uint32_t e = *reinterpret_cast<const uint32_t *>(ws + o + 8);
+            return make_uint2(align_bytes(q.y, q.x, lead), align_bytes(e, q.y, lead));
+        }
+
+        __device__ __forceinline__ void empty(int first) {
             if constexpr (F == F_Q6_K) {
                 // codes of group 8hh + 2k + gg, values l = 16gg + 8lh .. + 7: eight bytes of ql at 64hh + 16gg + 8lh (k
                 // even) and 32 on (odd), of qh at 128 + 32hh + 16gg + 8lh; pair p = 2hh + gg
+                const uint32_t lead = 2u * (uint32_t)((wodd + first) & 1);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     const int hh = p >> 1, gg = p & 1;
-                    const uint2 qa = *reinterpret_cast<const uint2 *>(ws + 64 * hh + 16 * gg + 8 * lh);
-                    const uint2 qb = *reinterpret_cast<const uint2 *>(ws + 64 * hh + 32 + 16 * gg + 8 * lh);
-                    const uint2 qh = *reinterpret_cast<const uint2 *>(ws + 128 + 32 * hh + 16 * gg + 8 * lh);
+                    const uint2 qa = rd8(64 * hh + 16 * gg + 8 * lh, lead);
+                    const uint2 qb = rd8(64 * hh + 32 + 16 * gg + 8 * lh, lead);
+                    const uint2 qh = rd8(128 + 32 * hh + 16 * gg + 8 * lh, lead);
                     v[6 * p] = qa.x, v[6 * p + 1] = qa.y, v[6 * p + 2] = qb.x, v[6 * p + 3] = qb.y;
                     v[6 * p + 4] = qh.x, v[6 * p + 5] = qh.y;
                 }
                 const uint4 s = rd16(ws + 192);
-                v[24] = s.x, v[25] = s.y, v[26] = s.z, v[27] = s.w;
-                v[28] = *reinterpret_cast<const uint16_t *>(ws + 16 * FULL + 14);     // d ends the super-block
+                const uint32_t end = *reinterpret_cast<const uint32_t *>(ws + 16 * FULL + 12);     // behind a lead two scales, d
+                v[24] = align_bytes(s.y, s.x, lead), v[25] = align_bytes(s.z, s.y, lead);
+                v[26] = align_bytes(s.w, s.z, lead), v[27] = align_bytes(end, s.w, lead);
+                v[28] = end >> (8 * lead);
             } else {
 #pragma unroll
                 for (int c = 0; c < NV / 4; ++c) {         // the head, then half of every 32 bytes of codes
@@ -93,7 +107,7 @@ struct SuperBlocks {
         }
         __device__ __forceinline__ int scale6(int g) const { return (int)(int8_t)(v[24 + g / 4] >> (8 * (g & 3))); }
 
-        __device__ __forceinline__ void work(const uint8_t *xs) {
+        __device__ __forceinline__ void work(const uint8_t *xs, int, int) {
             const uint8_t *xl = xs + XROW * (ROWS < 32 ? lane & (ROWS - 1) : lane & 31);     // rows past the tile's LDS rows repeat them
             if (lane < ROWS) d8w[lane] = *reinterpret_cast<const float *>(xs + XROW * lane + 288);
             auto codes = [&](int kt) {

@@ -361,6 +361,39 @@ def test_experts_128_rows_of_odd_blocks(env, fmt):
     _product(env, fmt, 2100, 2, 8, 24, 288, False, _ids(np.random.default_rng(3), 2100, 2, 8))
 
 
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0", "q4_1", "q5_0", "q5_1"])
+@pytest.mark.parametrize("T,top,E,N,per_pair", [
+    (40, 2, 64, 776, False), (20, 4, 16, 904, True), (33, 2, 16, 40, False),              # tiles of 16 rows, by workgroups
+    (200, 2, 16, 1800, True), (100, 2, 8, 1400, False), (300, 4, 16, 56, True), (5, 3, 6, 72, False),       # of 32
+    (300, 3, 20, 40, True), (90, 1, 2, 200, False)])                                      # of 32, few workgroups
+@pytest.mark.parametrize("blocks", [9, 10, 12, 15, 19, 31])
+def test_experts_part_of_a_stage(env, fmt, T, top, E, N, per_pair, blocks):
+    """Rows that are no whole number of 256 values: of an odd number of blocks, of an even one."""
+    _say("experts part", fmt, T, top, E, N, blocks, per_pair)
+    _product(env, fmt, T, top, E, N, 32 * blocks, per_pair, _ids(np.random.default_rng(T + blocks), T, top, E, skew=True))
+
+
+@pytest.mark.parametrize("fmt", ["q2_k", "q4_k", "q6_k"])
+@pytest.mark.parametrize("T", [30, 700, 1700])
+def test_experts_of_one_superblock(env, fmt, T):
+    _say("experts of one super-block", fmt, T)
+    _product(env, fmt, T, 3, 9, 136, 256, T == 700, _ids(np.random.default_rng(T), T, 3, 9, skew=True))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_experts_one_block(env, fmt):
+    """K of one block, with a plan."""
+    _say("experts of one block", fmt)
+    _product(env, fmt, 260, 2, 5, 70, 256 if fmt.endswith("_k") else 32, True, _ids(np.random.default_rng(8), 260, 2, 5))
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0", "q4_1", "q5_0", "q5_1"])
+@pytest.mark.parametrize("blocks", [9, 13, 14])
+def test_experts_128_rows_of_part_stages(env, fmt, blocks):
+    _say("experts part of a stage, 128 rows", fmt, blocks)
+    _product(env, fmt, 2090, 2, 7, 136, 32 * blocks, blocks == 13, _ids(np.random.default_rng(3), 2090, 2, 7, skew=True))
+
+
 @pytest.mark.parametrize("T", [9, 40, 300, 1500, 2500])
 @pytest.mark.parametrize("fmt", ["q4_0", "q4_k"])
 def test_experts_unusual_ids(env, fmt, T):
