@@ -517,7 +517,9 @@ qmm_status qmm_rms_norm_q8_k(const void *x, const void *residual, void *sum, con
                              int64_t sum_stride, int64_t y_stride, float eps, float weight_offset, void *stream);
 
 /* Gated activation and quantization, in one launch: xq = the blocks (as above) of
- * act(gate) * up, computed in f32 to a few units of its last place:
+ * act(gate) * up, computed in f32 to a few units of its last place (far down the GELUs'
+ * negative tail, where e^(-g^2 / 2) magnifies the rounding of its argument, to 2^-15
+ * of itself):
  *   QMM_GLU_SILU       g / (1 + e^-g)
  *   QMM_GLU_GELU       g/2 (1 + erf(g / sqrt 2))
  *   QMM_GLU_GELU_TANH  g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
@@ -539,14 +541,14 @@ qmm_status qmm_glu_q8_k(const void *gate, const void *up, void *xq8k, int dtype,
  *   weights = p of those, divided by their sum if renorm, times scale.
  * Equal c go to the lowest index, equal groups too.  An expert whose logit (or
  * bias) is -inf is never chosen, and where fewer than top_k can be, the rest of
- * the ids are -1 with weight 0.  A NaN counts as larger than any number and shows
- * in the weights.  Scores are f64, so the order is the formula's; without a bias
- * it is the logits' own.
+ * the ids are -1 with weight 0.  A NaN counts as larger than any number; that of a
+ * logit shows in the weights.  Scores are f64, so the order is the formula's; without
+ * a bias it is the logits' own.
  *   logits  : [T][E] in dtype, row t at t * logits_stride elements; any alignment
  *             and stride >= 0.
  *   bias    : f32 [E], or NULL.
  *   ids     : int32 [T][top_k], written.    weights : f32 [T][top_k], written.
- * top_k <= groups_kept * E/groups; groups <= 64. */
+ * top_k <= groups_kept * E/groups; groups <= 64; scale finite. */
 typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
 qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *ids, float *weights, int64_t T,
                      int64_t E, int64_t logits_stride, int64_t top_k, int score, int64_t groups, int64_t groups_kept,
@@ -572,7 +574,8 @@ qmm_status qmm_experts_plan(const int32_t *ids, void *plan, int64_t plan_bytes, 
  *          w + e * expert_stride bytes; expert_stride a multiple of 16
  *          (QMM_E_ALIGN otherwise), at least one matrix.
  *   xq   : x_rows rows of Q8_0 (K-quants: Q8_K) blocks, less than 4 GiB.
- *   ids, plan, plan_bytes : the ids that the plan was made of, and the plan.
+ *   ids, plan, plan_bytes : the ids that the plan was made of, and the plan (of
+ *          another plan's bytes come wrong rows, but no access outside the buffers).
  *   y    : f32 [T * top_k][N], written.
  * N <= 2^18, T * top_k * N <= 2^35, K as for qmm_matmul_*. */
 qmm_status qmm_experts_matmul_q4_0(const void *w, int64_t expert_stride, const void *xq, int64_t x_rows,

@@ -102,7 +102,7 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
     QMM_TRY(check_device());
     ExpertArgs a = {static_cast<const uint8_t *>(w), stride, static_cast<const uint8_t *>(xq),
                     (uint32_t)(x_rows * nb * xbytes), x_rows == pairs, y, nullptr, {}, (int)pairs, (int)top_k, (int)E,
-                    (int)N, (int)nb, tile_rows(pairs, E)};
+                    (int)N, (int)nb, (int)x_rows, tile_rows(pairs, E)};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (pairs <= kSelfPairs)
         a.ids = ids;
@@ -142,7 +142,7 @@ qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *
     if (!dtype_ok(dtype) || !pairs_ok(T, top_k, E) || top_k > E || T > kMaxTokens) return QMM_E_SHAPE;
     if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID) return QMM_E_SHAPE;
     if (groups < 1 || groups > kWave || E % groups != 0 || groups_kept < 1 || groups_kept > groups) return QMM_E_SHAPE;
-    if (top_k > E / groups * groups_kept || (group_top != 1 && group_top != 2) || std::isnan(scale)) return QMM_E_SHAPE;
+    if (top_k > E / groups * groups_kept || (group_top != 1 && group_top != 2) || !std::isfinite(scale)) return QMM_E_SHAPE;
     if (logits_stride < 0 || logits_stride > kMaxBytes || (__int128)(T - 1) * logits_stride + E > kMaxBytes / 4)
         return QMM_E_SHAPE;
     QMM_TRY(check_index(logits, row_type_bytes(dtype)));

@@ -43,11 +43,17 @@ template <int ROWS, int WPG, int XC, int WC, int XD> struct Layout {
 };
 }  // namespace es
 
+// A buffer's descriptor in scalar registers.
+__device__ __forceinline__ v4i stream_buffer(const uint8_t *p, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return v4i{uniform((int)(uint32_t)at), uniform((int)(uint32_t)(at >> 32) & 0xffff), uniform((int)bytes), 0x00020000};
+}
+
 // 16 bytes a lane from a buffer into LDS at m0base + 16 * lane; inline assembly, so
 // that the compiler does not wait for the copies in flight before each LDS read.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void stream_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t m0base, uint32_t voff, int soff) {
+__device__ __forceinline__ void stream_to_lds(v4i r, uint32_t m0base, uint32_t voff, int soff) {
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(m0base), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
 }
@@ -84,9 +90,8 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
     // up to two bytes past the last row, in its last dword
     const uint32_t x_bytes = C::XLEAD ? (rows.x_bytes + 3) & ~3u : rows.x_bytes;
     const uint32_t w_bytes = (uint32_t)min(a.N - n0, BN) * wrow;
-    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void *)a.x, 0, (int)x_bytes, 0x00020000);
-    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(w + (int64_t)n0 * wrow), 0, (int)(C::WLEAD ? (w_bytes + 3) & ~3u : w_bytes), 0x00020000);
+    const v4i xr = stream_buffer(a.x, x_bytes);
+    const v4i wr = stream_buffer(w + (int64_t)n0 * wrow, C::WLEAD ? (w_bytes + 3) & ~3u : w_bytes);
     // copies: rows past the matrix, and past the tile, repeat its last
     uint32_t xoff[L::NA], woff[L::WL], xat[L::NA];
     // what a stage that starts at an odd block adds: its scalar offset is two bytes less

@@ -5,7 +5,9 @@
 
 namespace qmm {
 
-// In f32, each within a few units of its last place; the result is held in 8 bits.
+// In f32, each within a few units of its last place, but for the GELUs' far negative
+// tail: e^(-z^2) with z^2 < 104 of a z rounded to 2^-24 of itself is off by up to 2 z^2
+// 2^-24 = 2^-16 of itself.  The result is held in 8 bits.
 template <int ACT>
 __device__ __forceinline__ float activation(float g) {
     if constexpr (ACT == G_SILU) return g / (1.0f + expf(-g));

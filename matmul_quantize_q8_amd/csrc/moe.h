@@ -86,6 +86,7 @@ struct ExpertArgs {
     const int *ids;             // [pairs]; with it instead of the plan: kSelfPairs at most
     Plan plan;
     int pairs, top, E, N, nb;   // nb: blocks of a row
+    int x_rows;                 // pairs, or tokens
     int rows;                   // rows of a tile
 };
 
@@ -132,8 +133,10 @@ struct TileRows {
 
 // Tile `chunk` of a product and its rows, into LDS tables of at least a.rows
 // entries: of the plan, or in a call without one the pairs of pair `chunk`'s
-// expert, if it is the first of every a.rows of them (count 0 otherwise).  The
-// caller has a barrier before the tables are read.
+// expert, if it is the first of every a.rows of them (count 0 otherwise).  What the
+// plan holds is kept inside the call's sizes: bytes that no plan of this size wrote
+// give wrong rows, but no access outside the buffers.  The caller has a barrier before
+// the tables are read.
 __device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int *pair, int *src) {
     Tile t;
     const int most = a.rows;
@@ -159,7 +162,8 @@ __device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int 
         }
         t = a.plan.tiles[chunk];
         t.expert = uniform(t.expert);
-        t.count = uniform(t.count);
+        t.count = (unsigned)t.expert > (unsigned)a.E ? 0 : max(min(uniform(t.count), most), 0);
+        p = (int)min((unsigned)p, (unsigned)a.pairs - 1), x = (int)min((unsigned)x, (unsigned)a.x_rows - 1);
         if ((int)threadIdx.x < t.count) pair[threadIdx.x] = p, src[threadIdx.x] = x;
     }
     return t;

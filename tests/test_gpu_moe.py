@@ -571,3 +571,179 @@ def test_on_another_stream(env):
         step()
     side.synchronize()
     assert torch.equal(b["out"], want)
+
+
+# ---------------------------------------------------------------------------
+# Further calls that the contracts allow
+# ---------------------------------------------------------------------------
+def _counted(torch, q, T, top, E, N=8, K=64):
+    """Matrices whose codes are all 1 with scale e + 1 and activations of whole numbers with scale 1: every product is
+    exact, (e + 1) times the sum of the row's codes, below 2^24."""
+    w = np.zeros((E, N, K // 32, 34), np.uint8)
+    w[..., :2] = (np.arange(E) + 1).astype(np.float16).view(np.uint8).reshape(E, 1, 1, 2)
+    w[..., 2:] = 1
+    codes = np.random.default_rng(T + E).integers(-127, 128, (T, K // 32, 32)).astype(np.int8)
+    x = np.zeros((T, K // 32, 34), np.uint8)
+    x[..., :2] = np.ones(1, np.float16).view(np.uint8)
+    x[..., 2:] = codes.view(np.uint8)
+    return (_dev(torch, w.reshape(E, N, -1)), _dev(torch, x.reshape(T, -1)), codes.astype(np.int64).sum((1, 2)))
+
+
+@pytest.mark.parametrize("skew", ["even", "one", "few", "none"])
+@pytest.mark.parametrize("E,top", [(512, 4), (65, 1), (1, 1), (3, 2)])
+@pytest.mark.parametrize("T", [600, 2100, 2600, 70001])
+def test_plan_of_many_pairs(env, T, E, top, skew):
+    """One segment, several, 256 of them; experts of every count, and all pairs with one or without any."""
+    torch, q, _ = env
+    _say("plan", T, E, top, skew)
+    rng = np.random.default_rng(T + E)
+    ids = rng.integers(0, E, (T, top)).astype(np.int32)
+    if skew == "one":
+        ids[:] = E - 1
+    elif skew == "few":
+        ids = np.minimum(ids, rng.integers(-1, 3, (T, top))).astype(np.int32)
+    elif skew == "none":
+        ids[rng.random((T, top)) < 0.9] = -7
+    w, x, sums = _counted(torch, q, T, top, E)
+    plan = q.experts_plan(T, top, E)
+    plan.fill_(0x55)
+    y = torch.full((T, top, 8), math.nan, device="cuda")
+    ids_d = _dev(torch, ids)
+    q.qmm_experts_plan(ids_d, E, plan)
+    q.qmm_experts_matmul_q8_0(w, x, ids_d, plan, y)
+    want = np.where((ids >= 0) & (ids < E), (ids + 1) * sums[:, None], 0)
+    assert np.array_equal(y.cpu().numpy(), np.repeat(want[..., None], 8, 2).astype(np.float32))
+
+
+@pytest.mark.parametrize("fmt,K", [("q4_0", 512), ("q8_0", 288), ("q5_1", 320), ("q4_1", 96), ("q2_k", 512), ("q6_k", 768)])
+@pytest.mark.parametrize("T", [1, 9, 60, 130, 700, 2300])
+def test_experts_other_rows_do_not_matter(env, fmt, K, T):
+    """A NaN row, and other contents, leave the bits of the rest."""
+    torch, q, orc = env
+    _say("other rows", fmt, T, K)
+    E, top, N = 5, 2, 40
+    rng = np.random.default_rng(T)
+    w, _ = _matrices(torch, orc, q, fmt, E, N, K, rng)
+    act = q.ACT_FORMAT[fmt]
+    xq = np.asarray(orc.quantize_x(fmt, rng.standard_normal((T, K)).astype(np.float32))).reshape(T, -1)
+    ids = _dev(torch, _ids(rng, T, top, E))
+    plan = q.experts_plan(T, top, E)
+    q.qmm_experts_plan(ids, E, plan)
+    out = []
+    for other in (False, True):
+        x = xq.copy()
+        if other:
+            x[::3] = x[::3][::-1]
+            x[1::7, :4] = 0xff                       # f16 and f32 NaN scales
+        y = torch.full((T, top, N), 7.0, device="cuda")
+        q.EXPERTS_MATMUL[fmt](w, _dev(torch, x), ids, plan, y)
+        out.append(y.cpu().numpy())
+    same = np.ones(T, bool)
+    same[::3] = same[1::7] = False
+    assert act in ("q8_0", "q8_k") and np.array_equal(out[0][same].view(np.uint32), out[1][same].view(np.uint32))
+    assert np.all(np.isnan(out[1][1::7]))
+    assert not np.isnan(out[0]).any()
+
+
+@pytest.mark.parametrize("fmt,K", [("q4_0", 512), ("q8_0", 288), ("q5_0", 64), ("q4_1", 32), ("q4_k", 512), ("q6_k", 768)])
+@pytest.mark.parametrize("T", [40, 130, 700, 2300])
+def test_experts_of_another_plan(env, fmt, K, T):
+    """The rows of a plan's bytes that are not of these ids stay inside y (the kernels keep them there)."""
+    torch, q, orc = env
+    _say("another plan", fmt, T, K)
+    E, top, N = 5, 2, 40
+    rng = np.random.default_rng(T)
+    w, _ = _matrices(torch, orc, q, fmt, E, N, K, rng)
+    xq = _dev(torch, np.asarray(orc.quantize_x(fmt, rng.standard_normal((T, K)).astype(np.float32))).reshape(T, -1))
+    ids = _dev(torch, _ids(rng, T, top, E))
+    plan = q.experts_plan(T, top, E)
+    room = torch.full((T * top + 512, N), 7.0, device="cuda")
+    y = room[256:-256]
+    for fill in (0x00, 0x01, 0x7f, 0x80, 0xff):
+        plan.fill_(fill)
+        q.EXPERTS_MATMUL[fmt](w, xq, ids, plan, y)
+        torch.cuda.synchronize()
+        assert torch.all(room[:256] == 7.0) and torch.all(room[-256:] == 7.0), fill
+    q.qmm_experts_plan(ids, E, plan)
+    q.EXPERTS_MATMUL[fmt](w, xq, ids, plan, y)
+    assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [96, 4096, 16416, 33024])
+def test_norm_in_place(env, dtype, K):
+    """sum over x, sum over the residual, y over x, y over the residual, against separate outputs; rows of stride 0."""
+    torch, q, _ = env
+    _say("norm in place", dtype, K)
+    T = 5
+    x = torch.randn(T, K, device="cuda").to(_t(torch, dtype))
+    r = torch.randn(T, K, device="cuda").to(_t(torch, dtype))
+    xq, s, y = (torch.empty(T, q.row_bytes("q8_0", K), dtype=torch.uint8, device="cuda"), torch.empty_like(x),
+                torch.empty_like(x))
+    q.qmm_rms_norm_q8_0(x, None, xq, residual=r, sum=s, y=y)
+    for names in (dict(sum="x"), dict(sum="r"), dict(y="x"), dict(y="r"), dict(sum="x", y="r"), dict(sum="r", y="x")):
+        b = dict(x=x.clone(), r=r.clone())
+        again = torch.empty_like(xq)
+        q.qmm_rms_norm_q8_0(b["x"], None, again, residual=b["r"], **{k: b[v] for k, v in names.items()})
+        assert torch.equal(again, xq), names
+        for k, v in names.items():
+            assert torch.equal(b[v], dict(sum=s, y=y)[k]), names
+    wide = torch.empty(T, xq.shape[1], dtype=torch.uint8, device="cuda")
+    q.qmm_rms_norm_q8_0(x[:1].expand(T, K), None, wide, residual=r[:1].expand(T, K))
+    assert torch.equal(wide, xq[:1].expand(T, -1))
+
+
+def test_two_streams_at_once(env):
+    """The same matrices on two streams, a plan each."""
+    torch, q, orc = env
+    _say("two streams")
+    E, top, N, K, T = 8, 2, 136, 512, 400
+    rng = np.random.default_rng(0)
+    w, _ = _matrices(torch, orc, q, "q4_0", E, N, K, rng)
+    sides = []
+    for n in range(2):
+        xq = _dev(torch, np.asarray(orc.quantize_x("q4_0", rng.standard_normal((T, K)).astype(np.float32))).reshape(T, -1))
+        sides.append(dict(ids=_dev(torch, _ids(rng, T, top, E)), xq=xq, plan=q.experts_plan(T, top, E),
+                          y=torch.empty(T, top, N, device="cuda"), stream=torch.cuda.Stream()))
+
+    def run(s, stream):
+        q.qmm_experts_plan(s["ids"], E, s["plan"], stream=stream)
+        q.qmm_experts_matmul_q4_0(w, s["xq"], s["ids"], s["plan"], s["y"], stream=stream)
+    want = []
+    for s in sides:
+        run(s, None)
+        want.append(s["y"].clone())
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in sides:
+            with torch.cuda.stream(s["stream"]):
+                s["y"].fill_(math.nan)
+            run(s, s["stream"])
+        torch.cuda.synchronize()
+        assert all(torch.equal(s["y"], v) for s, v in zip(sides, want))
+
+
+def test_two_graphs_by_turns(env):
+    """Two captured passes of different sizes, replayed by turns: nothing of one is left in the other."""
+    torch, q, orc = env
+    _say("two graphs")
+    made = []
+    for T in (20, 260):
+        b, step, _, _ = _block(torch, q, "q4_k", T, seed=T, orc=orc)
+        b["x"].normal_()
+        keep = b["stream"].normal_().clone()
+        step()
+        want = b["out"].clone()
+        b["stream"].copy_(keep)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        made.append((b, keep, want, graph, step))        # the pass holds the matrices
+    for _ in range(3):
+        for b, keep, want, graph, _ in made:
+            b["stream"].copy_(keep)
+            b["out"].fill_(math.nan)
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(b["out"], want) for b, _, want, _, _ in made)

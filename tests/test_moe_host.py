@@ -69,7 +69,7 @@ def route(q, **kw):
     (dict(E=512, top=64), NULL), (dict(E=512, top=65), SHAPE), (dict(top=0), SHAPE), (dict(E=8, top=9), SHAPE),
     (dict(score=2), SHAPE), (dict(groups=0), SHAPE), (dict(groups=7), SHAPE), (dict(groups=128, E=128), SHAPE),
     (dict(groups=8, kept=9), SHAPE), (dict(groups=8, kept=0), SHAPE), (dict(groups=8, kept=1), NULL),
-    (dict(groups=16, kept=1), SHAPE), (dict(group_top=3), SHAPE), (dict(group_top=0), SHAPE), (dict(scale=math.nan), SHAPE),
+    (dict(groups=16, kept=1), SHAPE), (dict(group_top=3), SHAPE), (dict(group_top=0), SHAPE), (dict(scale=math.nan), SHAPE), (dict(scale=math.inf), SHAPE), (dict(scale=-math.inf), SHAPE),
     (dict(stride=-1), SHAPE), (dict(stride=0), NULL), (dict(logits=None), NULL), (dict(logits=A + 2), ALIGN),
     (dict(logits=A + 2, dtype=2), NULL), (dict(ids=None), NULL), (dict(ids=A + 1), ALIGN), (dict(bias=A + 2, weights=A), ALIGN),
     (dict(bias=None), NULL), (dict(dtype=3), SHAPE)])
