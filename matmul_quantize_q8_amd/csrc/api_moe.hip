@@ -81,6 +81,23 @@ bool pairs_ok(int64_t T, int64_t top_k, int64_t E) {
     return T >= 1 && top_k >= 1 && top_k <= kMaxTop && E >= 1 && E <= kMaxExperts && T <= kMaxPairs / top_k;
 }
 
+// A plan's tiles of 128 rows as four of 32 each, where workgroups of 128 x 128 leave
+// compute units idle (us, whole / in parts, K = 1024; a round: 512 of them, two a
+// compute unit):
+//   8192 rows, 1 expert of 256      130  Q4_0 23 / 16, Q8_0 23 / 19, Q6_K 25 / 21, Q4_K 27 / 13
+//   16384 rows, 64 experts of 104   192  Q4_0 23 / 21, Q8_0 23 / 29, Q6_K 25 / 32, Q4_K 26 / 16
+//   16384 rows, 8 experts of 512    544  Q4_0 49 / 50, Q8_0 51 / 67, Q6_K 74 / 74, Q4_K 54 / 39
+//   16384 rows, 64 experts of 512   768  Q4_0 53 / 57, Q8_0 56 / 79, Q6_K 75 / 82, Q4_K 56 / 45
+//   8192 rows, 1 expert of 2048    1040  Q4_0 67 / 88, Q8_0 68 / 115, Q6_K 104 / 128, Q4_K 65 / 71
+// Q2_K and Q4_K, whose tiles of 32 are nearly as fast as those of 128, gain wherever
+// the last round is not nearly full.
+bool in_parts(int fmt, const ExpertArgs &a) {
+    const int64_t tiles = a.pairs / kFullRows + (a.pairs < a.E ? a.pairs : a.E) / 2;      // experts end in the middle of one
+    const int64_t blocks = tiles * ((a.N + 127) / 128), round = 2 * kCUs;
+    if (fmt == F_Q2_K || fmt == F_Q4_K) return 5 * blocks <= 4 * ((blocks + round - 1) / round * round);
+    return blocks <= kCUs / 2;
+}
+
 typedef hipError_t (*few_launch)(const ExpertArgs &, hipStream_t);
 
 qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride, const void *xq, int64_t x_rows,
@@ -111,7 +128,7 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
     // one token's experts have a row each: the decode product's way; a single block of 32
     // values is no stage of any other
     if (T == 1 || (!k && nb < 2)) return launched(few(a, st));
-    if (a.rows <= kNarrowRows && (k || experts_stream_32_suits(fmt, a)))
+    if ((a.rows <= kNarrowRows || in_parts(fmt, a)) && (k || experts_stream_32_suits(fmt, a)))
         return launched(k ? launch_experts_stream_k(fmt, a, st) : launch_experts_stream_32(fmt, a, st));
     return launched(k ? launch_experts_k(fmt, a, st) : launch_experts_32(fmt, a, st));
 }

@@ -32,7 +32,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_few(ExpertArgs a, in
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t row0 = ((int64_t)blockIdx.x * kFewWaves + wave) * RW;
     const int nrows = (int)max((int64_t)0, min((int64_t)RW, (int64_t)a.N - row0));
-    const Tile tile = expert_tile(a, tile0 + (int)blockIdx.y, pairs, sources);
+    const Tile tile = expert_tile(a, tile0 + (int)blockIdx.y, pairs, sources, 0, a.rows);
     if (tile.count == 0) return;
     __syncthreads();
     if (tile.expert == a.E) {                          // no expert: zeros

@@ -185,15 +185,16 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
 }
 
 template <class C, int ROWS, int G, int WPG>
-__global__ __launch_bounds__(64 * G * WPG) void k_experts_stream(ExpertArgs a, int tiles_n) {
+__global__ __launch_bounds__(64 * G * WPG) void k_experts_stream(ExpertArgs a, int tiles_n, int parts) {
     using L = typename C::template Lds<ROWS, WPG>;
     extern __shared__ __attribute__((aligned(16))) uint8_t stream_lds[];
     int *pair = reinterpret_cast<int *>(stream_lds + G * L::LDS), *src = pair + ROWS;
-    const int chunk = (int)blockIdx.x / tiles_n;
-    const Tile tile = expert_tile(a, chunk, pair, src);
+    // parts: log2 of the workgroups that a tile's rows take
+    const int part = (int)blockIdx.x / tiles_n, chunk = part >> parts;
+    const Tile tile = expert_tile(a, chunk, pair, src, (part - (chunk << parts)) * ROWS, ROWS);
     if (tile.count == 0) return;
     __syncthreads();
-    const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};
+    const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - part * tiles_n};
     if (tile.expert == a.E) {
         zero_tile(a, tile.count, rows, 32 * WPG);
         return;
@@ -215,16 +216,17 @@ static hipError_t launch_stream(const ExpertArgs &a, hipStream_t st) {
     static int lds_ok[kLdsDevices] = {};
     const hipError_t e = allow_dynamic_lds(k, (size_t)lds, lds_ok);
     if (e != hipSuccess) return e;
-    int tiles_n = (a.N + 32 * WPG - 1) / (32 * WPG);
+    int tiles_n = (a.N + 32 * WPG - 1) / (32 * WPG), parts = 0;
+    while (ROWS << parts < a.rows) ++parts;
     ExpertArgs args = a;
-    void *argv[] = {(void *)&args, (void *)&tiles_n};
-    return hipLaunchKernel(k, dim3((unsigned)(grid_tiles(a) * tiles_n)), dim3(64 * G * WPG), argv, (size_t)lds, st);
+    void *argv[] = {(void *)&args, (void *)&tiles_n, (void *)&parts};
+    return hipLaunchKernel(k, dim3((unsigned)((grid_tiles(a) << parts) * tiles_n)), dim3(64 * G * WPG), argv, (size_t)lds, st);
 }
 
 // Blocks of 128 weight rows that the call is likely to have, every expert in use.
 constexpr int64_t kEnoughBlocks = 3 * kCUs / 2, kFewBlocks = kCUs / 2;       // for one group of waves each; for no two
 inline int64_t stream_blocks(const ExpertArgs &a) {
-    const int64_t tiles = (a.pairs < a.E ? a.pairs : a.E) + a.pairs / a.rows;
+    const int64_t tiles = (a.pairs < a.E ? a.pairs : a.E) + a.pairs / (a.rows < kNarrowRows ? a.rows : kNarrowRows);
     return tiles * ((a.N + 127) / 128);
 }
 
@@ -243,7 +245,6 @@ static hipError_t pick_stream(const ExpertArgs &a, hipStream_t st) {
 
 template <class C>
 static hipError_t experts_stream(const ExpertArgs &a, hipStream_t st) {
-    if (a.rows > kNarrowRows) return hipErrorInvalidValue;             // the kernel's tables
     return a.rows <= kFewRows ? pick_stream<C, kFewRows>(a, st) : pick_stream<C, kNarrowRows>(a, st);
 }
 

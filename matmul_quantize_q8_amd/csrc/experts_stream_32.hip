@@ -266,7 +266,6 @@ static hipError_t pick(const ExpertArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_experts_stream_32(int fmt, const ExpertArgs &a, hipStream_t st) {
-    if (a.rows > kNarrowRows) return hipErrorInvalidValue;             // the kernel's tables
     switch (fmt) {
         case F_Q4_0: return pick<F_Q4_0>(a, st);
         case F_Q8_0: return pick<F_Q8_0>(a, st);

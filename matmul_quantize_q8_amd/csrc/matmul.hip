@@ -892,7 +892,7 @@ __global__ __launch_bounds__(mm::NT, 2) void k_experts_matmul(ExpertArgs a, int 
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
     __shared__ int pair[MOST], src[MOST];
     const int chunk = (int)blockIdx.x / tiles_n;
-    const Tile tile = expert_tile(a, chunk, pair, src);
+    const Tile tile = expert_tile(a, chunk, pair, src, 0, a.rows);
     if (tile.count == 0) return;
     __syncthreads();
     const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};

@@ -680,7 +680,7 @@ __global__ __launch_bounds__(mk::NT) void k_experts_matmul_k(ExpertArgs a, int t
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     int *pair = reinterpret_cast<int *>(lds + mk::KW<F>::LDS_BYTES), *src = pair + kFullRows;
     const int chunk = (int)blockIdx.x / tiles_n;
-    const Tile tile = expert_tile(a, chunk, pair, src);
+    const Tile tile = expert_tile(a, chunk, pair, src, 0, a.rows);
     if (tile.count == 0) return;
     __syncthreads();
     const TileRows rows = {pair, src, a.x_bytes, (int)blockIdx.x - chunk * tiles_n};

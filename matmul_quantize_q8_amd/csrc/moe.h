@@ -131,15 +131,15 @@ struct TileRows {
     int nt;                     // which columns of the output
 };
 
-// Tile `chunk` of a product and its rows, into LDS tables of at least a.rows
-// entries: of the plan, or in a call without one the pairs of pair `chunk`'s
-// expert, if it is the first of every a.rows of them (count 0 otherwise).  What the
+// Rows from .. from + most - 1 of tile `chunk` of a product, into LDS tables of `most`
+// entries: of the plan, or in a call without one (from 0, most a.rows) the pairs of pair
+// `chunk`'s expert, if it is the first of every a.rows of them.  count: those that there
+// are.  What the
 // plan holds is kept inside the call's sizes: bytes that no plan of this size wrote
 // give wrong rows, but no access outside the buffers.  The caller has a barrier before
 // the tables are read.
-__device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int *pair, int *src) {
+__device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int *pair, int *src, int from, int most) {
     Tile t;
-    const int most = a.rows;
     if (a.ids != nullptr) {
         const int lane = threadIdx.x & 63, id = lane < a.pairs ? a.ids[lane] : -1;
         const int e = __builtin_amdgcn_readlane(id, chunk);
@@ -157,12 +157,13 @@ __device__ __forceinline__ Tile expert_tile(const ExpertArgs &a, int chunk, int 
         // loaded beside the tile: rows past its count are whatever the plan holds
         int p = 0, x = 0;
         if ((int)threadIdx.x < most) {
-            p = a.plan.pair[(int64_t)chunk * most + threadIdx.x];
-            x = a.x_per_pair ? p : a.plan.token[(int64_t)chunk * most + threadIdx.x];
+            const int64_t at = (int64_t)chunk * a.rows + from + threadIdx.x;
+            p = a.plan.pair[at];
+            x = a.x_per_pair ? p : a.plan.token[at];
         }
         t = a.plan.tiles[chunk];
         t.expert = uniform(t.expert);
-        t.count = (unsigned)t.expert > (unsigned)a.E ? 0 : max(min(uniform(t.count), most), 0);
+        t.count = (unsigned)t.expert > (unsigned)a.E ? 0 : max(min(min(uniform(t.count), a.rows) - from, most), 0);
         p = (int)min((unsigned)p, (unsigned)a.pairs - 1), x = (int)min((unsigned)x, (unsigned)a.x_rows - 1);
         if ((int)threadIdx.x < t.count) pair[threadIdx.x] = p, src[threadIdx.x] = x;
     }

@@ -394,6 +394,16 @@ def test_experts_128_rows_of_part_stages(env, fmt, blocks):
     _product(env, fmt, 2090, 2, 7, 136, 32 * blocks, blocks == 13, _ids(np.random.default_rng(3), 2090, 2, 7, skew=True))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,top,E,N,K,per_pair", [(2200, 2, 7, 72, 768, False), (2300, 2, 5, 300, 512, True),
+                                                  (4200, 1, 1, 1400, 256, False), (2500, 2, 4, 2600, 256, True)])
+def test_experts_tiles_of_128_in_parts(env, fmt, T, top, E, N, K, per_pair):
+    """Few columns, and more, at many rows an expert."""
+    torch, q, orc = env
+    _say("experts parts", fmt, T, top, E, N, K, per_pair)
+    _product(env, fmt, T, top, E, N, K, per_pair, _ids(np.random.default_rng(T), T, top, E, skew=True))
+
+
 @pytest.mark.parametrize("T", [9, 40, 300, 1500, 2500])
 @pytest.mark.parametrize("fmt", ["q4_0", "q4_k"])
 def test_experts_unusual_ids(env, fmt, T):
