@@ -7,7 +7,9 @@
 // bytes of its rows into its own LDS slice and dots them with the activation rows
 // in turn.  LPR lanes share a weight row, each holding one unit of it and of the
 // activations (units as in the decode matvec), so that experts' short rows fill a
-// wave too; rows of more than 64 units are walked in segments.
+// wave too; rows of more than 64 units are walked in segments.  (8 of 128 experts of
+// 1536 x 2048: Q4_0 4.8 us, 3.0 TB/s of weights; Q8_0 5.7 us, 4.7 TB/s; about 2 us of
+// each are the launch and the chain from the ids to the first weight byte.)
 #include "matvec_kernel.h"
 #include "moe.h"
 

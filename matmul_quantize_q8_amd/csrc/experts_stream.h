@@ -13,8 +13,8 @@
 //     registers at the start of a step and at once copies the next stage into it:
 //     a stage is on its way during all of a step, at half the LDS of two buffers,
 //     and three or four workgroups share a compute unit (128 experts of
-//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 27.7 us, 64 tokens 54.7 ->
-//     47.7; Q8_0, 64 tokens 117 -> 77).  Only the activations, which the waves
+//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 26.5 us, 64 tokens 54.7 ->
+//     44.7; Q8_0, 64 tokens 117 -> 76, which is 4.8 TB/s of weights).  Only the activations, which the waves
 //     share, have two buffers.
 //   * Tiles of 16 rows where an expert has few: less LDS, less of the fold.
 //

@@ -883,8 +883,12 @@ __global__ __launch_bounds__(mm::NT, 2) void k_matmul_narrow(const uint8_t *__re
 }
 
 // The experts' products: a tile of the plan and 128 weight rows of its expert to
-// a workgroup, consecutive workgroups on the same rows.  Tiles of up to 32 rows come
-// here only where rows are no whole stages of 256 values.
+// a workgroup, consecutive workgroups on the same rows.  Bound as the prefill matmul is,
+// by the fold; the gathered rows, the chain from the plan to the first copy and the
+// tiles that an expert's rows do not fill cost the rest (Q4_0, 8192 rows of one expert
+// of 4096 x 1536 170 us, the matmul 164; 32768 rows of 64 experts of 1536 x 2048 358,
+// 577 TOPS).  Tiles of up to 32 rows come here only where rows are no whole stages of
+// 256 values (experts_stream_32.hip has the others).
 template <int WFMT, bool NARROW>
 __global__ __launch_bounds__(mm::NT, 2) void k_experts_matmul(ExpertArgs a, int tiles_n) {
     constexpr int LDS = NARROW ? mm::WN<WFMT>::template LDS_BYTES<1> : mm::WF<WFMT>::LDS_BYTES;
