@@ -25,7 +25,7 @@ hipError_t launch_experts_stream_32(int fmt, const ExpertArgs &a, hipStream_t st
 bool experts_stream_32_suits(int fmt, const ExpertArgs &a);
 hipError_t launch_experts_stream_k(int fmt, const ExpertArgs &a, hipStream_t st);
 hipError_t launch_experts_32(int fmt, const ExpertArgs &a, hipStream_t st);
-hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st);
+hipError_t launch_experts_q6_k(const ExpertArgs &a, hipStream_t st);
 int64_t matmul_q4_0_max_blocks();
 int64_t matmul_k_max_blocks();
 }  // namespace qmm
@@ -82,20 +82,13 @@ bool pairs_ok(int64_t T, int64_t top_k, int64_t E) {
 }
 
 // A plan's tiles of 128 rows as four of 32 each, where workgroups of 128 x 128 leave
-// compute units idle (us, whole / in parts, K = 1024; a round: 512 of them, two a
-// compute unit):
-//   8192 rows, 1 expert of 256      130  Q4_0 23 / 16, Q8_0 23 / 19, Q6_K 25 / 21, Q4_K 27 / 13
-//   16384 rows, 64 experts of 104   192  Q4_0 23 / 21, Q8_0 23 / 29, Q6_K 25 / 32, Q4_K 26 / 16
-//   16384 rows, 8 experts of 512    544  Q4_0 49 / 50, Q8_0 51 / 67, Q6_K 74 / 74, Q4_K 54 / 39
-//   16384 rows, 64 experts of 512   768  Q4_0 53 / 57, Q8_0 56 / 79, Q6_K 75 / 82, Q4_K 56 / 45
-//   8192 rows, 1 expert of 2048    1040  Q4_0 67 / 88, Q8_0 68 / 115, Q6_K 104 / 128, Q4_K 65 / 71
-// Q2_K and Q4_K, whose tiles of 32 are nearly as fast as those of 128, gain wherever
-// the last round is not nearly full.
-bool in_parts(int fmt, const ExpertArgs &a) {
+// compute units idle (us, whole / in parts, K = 1024):
+//   8192 rows, 1 expert of 256      128 blocks  Q4_0 23 / 16, Q8_0 23 / 19, Q5_1 28 / 23
+//   16384 rows, 64 experts of 104   192         Q4_0 23 / 21, Q8_0 23 / 29, Q5_1 28 / 35
+//   8192 rows, 1 expert of 512      256         Q4_0 25 / 27, Q8_0 25 / 33, Q5_1 31 / 41
+bool in_parts(const ExpertArgs &a) {
     const int64_t tiles = a.pairs / kFullRows + (a.pairs < a.E ? a.pairs : a.E) / 2;      // experts end in the middle of one
-    const int64_t blocks = tiles * ((a.N + 127) / 128), round = 2 * kCUs;
-    if (fmt == F_Q2_K || fmt == F_Q4_K) return 5 * blocks <= 4 * ((blocks + round - 1) / round * round);
-    return blocks <= kCUs / 2;
+    return tiles * ((a.N + 127) / 128) <= kCUs / 2;
 }
 
 typedef hipError_t (*few_launch)(const ExpertArgs &, hipStream_t);
@@ -128,9 +121,12 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
     // one token's experts have a row each: the decode product's way; a single block of 32
     // values is no stage of any other
     if (T == 1 || (!k && nb < 2)) return launched(few(a, st));
-    if ((a.rows <= kNarrowRows || in_parts(fmt, a)) && (k || experts_stream_32_suits(fmt, a)))
-        return launched(k ? launch_experts_stream_k(fmt, a, st) : launch_experts_stream_32(fmt, a, st));
-    return launched(k ? launch_experts_k(fmt, a, st) : launch_experts_32(fmt, a, st));
+    // Q6_K, 64 experts of 1536 x 2048 with 192 / 256 / 512 / 1024 rows each, in tiles of 64 249 / 314 / 580 / 1112 us, of 128
+    // 263 / 325 / 567 / 1045
+    if (fmt == F_Q6_K && pairs / E >= 384 && !in_parts(a)) return launched(launch_experts_q6_k(a, st));
+    if (k) return launched(launch_experts_stream_k(fmt, a, st));
+    const bool stages = (a.rows < kFullRows || in_parts(a)) && experts_stream_32_suits(fmt, a);
+    return launched(stages ? launch_experts_stream_32(fmt, a, st) : launch_experts_32(fmt, a, st));
 }
 
 }  // namespace

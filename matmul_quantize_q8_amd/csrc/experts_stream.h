@@ -1,8 +1,12 @@
-// Experts' products of up to 32 rows a tile on MFMA: what the 32-value formats
-// (experts_stream_32.hip) and the K-quants (experts_stream_k.hip) share.
+// Experts' products of up to 64 rows a tile on MFMA: what the 32-value formats
+// (experts_stream_32.hip) and the K-quants (experts_stream_k.hip) share.  The K-quants'
+// products of many rows are here too: two workgroups a compute unit cover one another's
+// start, which one of the prefill matmul's 128 x 256 tiles a compute unit does not (64
+// experts of 1536 x 2048, 512 rows each: Q2_K 244 us, those tiles 259; Q4_K 320 / 349;
+// Q6_K 580 / 567, of 2048 x 768 319 / 348).
 //
-// Bound by the weight stream: with a few rows a tile every weight byte is used for
-// little work, so what counts is how many bytes are on their way.
+// Bound by the weight stream, where an expert has few rows: every weight byte is used
+// for little work, so what counts is how many bytes are on their way.
 //   * A stage is 256 values of every row: a weight row's part (84 bytes of Q2_K ..
 //     272 of Q8_0) is copied in 16-byte chunks, consecutive lanes on consecutive
 //     chunks, and one barrier, one wait and one chain of LDS reads serve all of it.
@@ -19,7 +23,7 @@
 //   * Tiles of 16 rows where an expert has few: less LDS, less of the fold.
 //
 // A workgroup: a tile's rows x 32 WPG weight rows, wave w of a group alone on weight
-// rows 32 w .., one 32 x 32 MFMA tile a step of K; G groups of WPG waves, each on
+// rows 32 w .., one 32 x 32 MFMA tile a step of K (two, of rows 32 .. 63); G groups of WPG waves, each on
 // its part of K, which join in LDS in a fixed order.
 #pragma once
 
@@ -37,7 +41,7 @@ constexpr float kBias = 12582912.0f;               // 1.5 * 2^23, bit pattern 0x
 // of WC chunks a stage; XD bytes of a wave's own.
 template <int ROWS, int WPG, int XC, int WC, int XD> struct Layout {
     static constexpr int WL = (32 * WC + kWave - 1) / kWave;  // wave loads of a wave's 32 weight rows
-    static constexpr int XL = (ROWS * XC + kWave - 1) / kWave, NA = (XL + WPG - 1) / WPG;    // of the activations; of those a wave's
+    static constexpr int XL = (ROWS * XC + kWave - 1) / kWave;       // of the activations
     static constexpr int XAREA = XL * 1024, WAREA = WL * 1024;
     static constexpr int WAT = 2 * XAREA, DXAT = WAT + WPG * WAREA, OWN = XD, LDS = DXAT + WPG * XD;
 };
@@ -93,12 +97,14 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
     const v4i xr = stream_buffer(a.x, x_bytes);
     const v4i wr = stream_buffer(w + (int64_t)n0 * wrow, C::WLEAD ? (w_bytes + 3) & ~3u : w_bytes);
     // copies: rows past the matrix, and past the tile, repeat its last
-    uint32_t xoff[L::NA], woff[L::WL], xat[L::NA];
+    // (activations: the 8 FR rows that are worked out)
+    constexpr int XL = (8 * FR * C::XC + kWave - 1) / kWave, NA = (XL + WPG - 1) / WPG;
+    uint32_t xoff[NA], woff[L::WL], xat[NA];
     // what a stage that starts at an odd block adds: its scalar offset is two bytes less
-    int xstep[C::XLEAD ? L::NA : 1], wstep[C::WLEAD ? L::WL : 1];
+    int xstep[C::XLEAD ? NA : 1], wstep[C::WLEAD ? L::WL : 1];
 #pragma unroll
-    for (int k = 0; k < L::NA; ++k) {
-        const int q = min(wave + WPG * k, L::XL - 1), f = min(kWave * q + lane, ROWS * C::XC - 1), row = f / C::XC;
+    for (int k = 0; k < NA; ++k) {
+        const int q = min(wave + WPG * k, XL - 1), f = min(kWave * q + lane, 8 * FR * C::XC - 1), row = f / C::XC;
         const int c = f - C::XC * row;
         const uint32_t r = (uint32_t)rows.src[min(row, M - 1)];
         xoff[k] = r * xrow + (uint32_t)C::xchunk(c);
@@ -134,7 +140,7 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
     auto copy_rows = [&](int s, int buffer) {
         const int at = first(s);
 #pragma unroll
-        for (int k = 0; k < L::NA; ++k)
+        for (int k = 0; k < NA; ++k)
             stream_to_lds(xr, (uint32_t)uniform((int)(lds0 + buffer * L::XAREA + xat[k])),
                           C::XLEAD && (at & 1) ? xoff[k] + xstep[C::XLEAD ? k : 0] : xoff[k],
                           C::XLEAD ? at * XB & ~3 : at * XB);
@@ -161,19 +167,20 @@ __device__ __forceinline__ void stream_tile(uint8_t *lds_all, const ExpertArgs &
     if constexpr (G > 1) {
         // the other groups hand their sums to group 0 through LDS, which adds them in
         // the groups' order
-        static_assert((G - 1) * WPG * 4096 <= G * L::LDS, "the sums fit");
-        float *sums = reinterpret_cast<float *>(lds_all) + 1024 * wave + lane;
+        constexpr int SUMS = 256 * FR;                     // of a wave
+        static_assert((G - 1) * WPG * SUMS * 4 <= G * L::LDS, "the sums fit");
+        float *sums = reinterpret_cast<float *>(lds_all) + SUMS * wave + lane;
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (grp > 0) {
 #pragma unroll
-            for (int r = 0; r < 4 * FR; ++r) sums[1024 * WPG * (grp - 1) + 64 * r] = step.acc[r];
+            for (int r = 0; r < 4 * FR; ++r) sums[SUMS * WPG * (grp - 1) + 64 * r] = step.acc[r];
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (grp > 0) return;
 #pragma unroll
         for (int g = 1; g < G; ++g)
 #pragma unroll
-            for (int r = 0; r < 4 * FR; ++r) step.acc[r] += sums[1024 * WPG * (g - 1) + 64 * r];
+            for (int r = 0; r < 4 * FR; ++r) step.acc[r] += sums[SUMS * WPG * (g - 1) + 64 * r];
     }
     const int n = n0 + 32 * wave + lr;                     // lane l, register r: row 8 (r / 4) + 4 (l / 32) + r % 4
     if (n >= a.N) return;
@@ -204,8 +211,12 @@ __global__ __launch_bounds__(64 * G * WPG) void k_experts_stream(ExpertArgs a, i
         stream_tile<C, ROWS, 1, G, WPG>(stream_lds, a, w, tile.count, rows);
     else if (ROWS == 16 || tile.count <= 16)
         stream_tile<C, ROWS, 2, G, WPG>(stream_lds, a, w, tile.count, rows);
+    else if (ROWS == 32 || tile.count <= 32)
+        stream_tile<C, ROWS, 4, G, WPG>(stream_lds, a, w, tile.count, rows);
+    else if (tile.count <= 48)
+        stream_tile<C, ROWS, ROWS == 64 ? 6 : 4, G, WPG>(stream_lds, a, w, tile.count, rows);
     else
-        stream_tile<C, ROWS, ROWS / 8, G, WPG>(stream_lds, a, w, tile.count, rows);
+        stream_tile<C, ROWS, ROWS == 64 ? 8 : 4, G, WPG>(stream_lds, a, w, tile.count, rows);
 }
 
 template <class C, int ROWS, int G, int WPG>
@@ -245,7 +256,14 @@ static hipError_t pick_stream(const ExpertArgs &a, hipStream_t st) {
 
 template <class C>
 static hipError_t experts_stream(const ExpertArgs &a, hipStream_t st) {
-    return a.rows <= kFewRows ? pick_stream<C, kFewRows>(a, st) : pick_stream<C, kNarrowRows>(a, st);
+    if (a.rows <= kFewRows) return pick_stream<C, kFewRows>(a, st);
+    // The K-quants' tiles of 128 in parts of 64 rows, or of 32: half of the weights' ways through LDS, half of the
+    // workgroups (us, 32 / 64 rows: 128 experts of 1536 x 2048, 64 rows each Q4_K 125 / 118, Q6_K 233 / 202; 64 of 512 rows
+    // each Q2_K 263 / 244, Q4_K 359 / 320, Q6_K 687 / 580; 8 of 3584 x 4096, 50 rows each, 560 blocks Q4_K 37 / 39, Q6_K
+    // 64 / 77)
+    if constexpr (C::HALF)
+        if (a.rows == kFullRows && stream_blocks(a) >= 2 * kEnoughBlocks) return launch_stream<C, kHalfRows, 1, 4>(a, st);
+    return pick_stream<C, kNarrowRows>(a, st);
 }
 
 }  // namespace qmm

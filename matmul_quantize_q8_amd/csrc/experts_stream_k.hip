@@ -20,6 +20,7 @@ template <int F>
 struct SuperBlocks {
     static constexpr int WBYTES = F == F_Q2_K ? kQ2KBytes : F == F_Q4_K ? kQ4KBytes : kQ6KBytes;
     static constexpr int BLOCKS = 1, XBYTES = kQ8KBytes;
+    static constexpr bool HALF = true;
     static constexpr bool TAIL = false, XLEAD = false, WLEAD = F == F_Q6_K;         // the others' bytes are whole dwords
     static constexpr int MORE = 2;                            // no chunk after a part's last
     // activation row: the codes in 16 chunks, the block sums in two, the chunk that starts with d
@@ -44,12 +45,15 @@ struct SuperBlocks {
         // scales (with d and dmin), then the code bytes that the lane's half feeds
         static constexpr int NV = F == F_Q2_K ? 13 : F == F_Q4_K ? 20 : 29;
         uint32_t v[NV];
-        float acc[16];
+        static constexpr int NT = FR > 4 ? 2 : 1;          // MFMA tiles of 32 rows
+        float acc[16 * NT];
 
         __device__ __forceinline__ Step(const uint8_t *w, uint8_t *own, int l)
             : ws(w), d8w(reinterpret_cast<float *>(own)), lane(l), lh(l >> 5) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) bias[r] = 0x4B400000, acc[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) bias[r] = 0x4B400000;
+#pragma unroll
+            for (int r = 0; r < 16 * NT; ++r) acc[r] = 0.0f;
         }
         static __device__ __forceinline__ uint4 rd16(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
         static __device__ __forceinline__ float half_lo(uint32_t x) { return f16_bits_to_f32(x); }
@@ -108,16 +112,19 @@ struct SuperBlocks {
         __device__ __forceinline__ int scale6(int g) const { return (int)(int8_t)(v[24 + g / 4] >> (8 * (g & 3))); }
 
         __device__ __forceinline__ void work(const uint8_t *xs, int, int) {
-            const uint8_t *xl = xs + XROW * (ROWS < 32 ? lane & (ROWS - 1) : lane & 31);     // rows past the tile's LDS rows repeat them
-            if (lane < ROWS) d8w[lane] = *reinterpret_cast<const float *>(xs + XROW * lane + 288);
-            auto codes = [&](int kt) {
-                const uint4 c = rd16(xl + 32 * kt + 16 * lh);
+            const int xrow = lane & (ROWS < 32 ? ROWS - 1 : 31);               // rows past the tile's LDS rows repeat them
+            auto xl = [&](int t) { return xs + XROW * (xrow + 32 * t); };      // of MFMA tile t
+            if (lane < 8 * FR) d8w[lane] = *reinterpret_cast<const float *>(xs + XROW * lane + 288);
+            auto codes = [&](int kt, int t) {
+                const uint4 c = rd16(xl(t) + 32 * kt + 16 * lh);
                 return v4i{(int)c.x, (int)c.y, (int)c.z, (int)c.w};
             };
-            v16f mn;
+            v16f mn[NT];
             if constexpr (F == F_Q2_K) {
                 const uint32_t scl[4] = {v[0], v[1], v[2], v[3]};
-                v16i V = bias;
+                v16i V[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) V[t] = bias;
 #pragma unroll
                 for (int kt = 0; kt < 8; ++kt) {
                     // K-step kt: group 2kt + lh, codes by a table of 0, sc, 2sc, 3sc
@@ -130,7 +137,8 @@ struct SuperBlocks {
                         const uint32_t q = v[4 + 4 * (kt >> 2) + e];
                         b[e] = (int)__builtin_amdgcn_perm(0u, tab, (q >> sft) & 0x03030303u);
                     }
-                    V = __builtin_amdgcn_mfma_i32_32x32x32_i8(codes(kt), b, V, 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) V[t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(codes(kt, t), b, V[t], 0, 0, 0);
                 }
                 const uint32_t mlo = lh ? v[2] : v[0], mhi = lh ? v[3] : v[1];        // groups 8h .. 8h + 7
                 v8h bm;
@@ -139,14 +147,15 @@ struct SuperBlocks {
                     bm[e] = (_Float16)(int)((mlo >> (8 * e + 4)) & 15u);
                     bm[4 + e] = (_Float16)(int)((mhi >> (8 * e + 4)) & 15u);
                 }
-                mn = sums(xl, bm);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mn[t] = sums(xl(t), bm);
                 const uint32_t dd = v[12];
                 float dw = half_lo(dd), ndm = -half_lo(dd >> 16);
                 asm volatile("" : "+v"(dw), "+v"(ndm));
                 const float nbw = dw * -es::kBias;         // exact: 11 + 2 significant bits
                 fold([&](int r) {
-                    const int e = V[r];
-                    return fmaf(ndm, mn[r], fmaf(__int_as_float(e), dw, nbw));
+                    const int e = V[r / 16][r % 16];
+                    return fmaf(ndm, mn[r / 16][r % 16], fmaf(__int_as_float(e), dw, nbw));
                 });
             } else if constexpr (F == F_Q4_K) {
                 int sc[8], mm[8];
@@ -157,7 +166,7 @@ struct SuperBlocks {
                     sc[j] = (int)(j < 4 ? A & 63u : (C & 15u) | ((A >> 6) << 4));
                     mm[j] = (int)(j < 4 ? B & 63u : (C >> 4) | ((B >> 6) << 4));
                 }
-                v16i A1 = {}, A2 = {};
+                v16i A1[NT] = {}, A2[NT] = {};
 #pragma unroll
                 for (int kt = 0; kt < 8; ++kt) {
                     const uint32_t sft = 4u * (uint32_t)(kt & 1);
@@ -171,44 +180,55 @@ struct SuperBlocks {
                         b1[e] = __builtin_bit_cast(int, nib * sh2);
                         b2[e] = __builtin_bit_cast(int, nib * sl2);
                     }
-                    const v4i x = codes(kt);
-                    A1 = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, b1, A1, 0, 0, 0);
-                    A2 = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, b2, A2, 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const v4i x = codes(kt, t);
+                        A1[t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, b1, A1[t], 0, 0, 0);
+                        A2[t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, b2, A2[t], 0, 0, 0);
+                    }
                 }
                 v8h bm;                                    // groups 8h .. 8h + 7: sub-blocks 4h .. 4h + 3, two groups each
 #pragma unroll
                 for (int e = 0; e < 8; ++e) bm[e] = (_Float16)(lh ? mm[4 + (e >> 1)] : mm[e >> 1]);
-                mn = sums(xl, bm);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mn[t] = sums(xl(t), bm);
                 float dw = half_lo(v[0]), ndm = -half_lo(v[0] >> 16);
                 asm volatile("" : "+v"(dw), "+v"(ndm));
-                fold([&](int r) { return fmaf(ndm, mn[r], (float)(A1[r] * 8 + A2[r]) * dw); });
+                fold([&](int r) {
+                    const int t = r / 16, k = r % 16;
+                    return fmaf(ndm, mn[t][k], (float)(A1[t][k] * 8 + A2[t][k]) * dw);
+                });
             } else {
                 int V[4 * FR];
 #pragma unroll
                 for (int r = 0; r < 4 * FR; ++r) V[r] = 0;
                 auto group = [](int t) { return 8 * (t >> 3) + 2 * (t & 3) + ((t >> 2) & 1); };
-                auto product = [&](int t) {                // step t = 4 (2hh + gg) + k
-                    const int p = t >> 2, k = t & 3;
-                    const uint32_t nsh = 4u * (uint32_t)(k >> 1), hsh = 2u * (uint32_t)k;
-                    const uint32_t l0 = v[6 * p + 2 * (k & 1)], l1 = v[6 * p + 2 * (k & 1) + 1];
-                    const uint32_t b0 = ((l0 >> nsh) & 0x0f0f0f0fu) | (((v[6 * p + 4] >> hsh) & 0x03030303u) << 4);
-                    const uint32_t b1 = ((l1 >> nsh) & 0x0f0f0f0fu) | (((v[6 * p + 5] >> hsh) & 0x03030303u) << 4);
-                    const uint2 x = *reinterpret_cast<const uint2 *>(xl + 16 * group(t) + 8 * lh);
+                uint32_t b0 = 0, b1 = 0;
+                auto product = [&](int u) {                // step u = NT (4 (2hh + gg) + k) + MFMA tile
+                    const int s = u / NT, t = u % NT, p = s >> 2, k = s & 3;
+                    if (t == 0) {
+                        const uint32_t nsh = 4u * (uint32_t)(k >> 1), hsh = 2u * (uint32_t)k;
+                        const uint32_t l0 = v[6 * p + 2 * (k & 1)], l1 = v[6 * p + 2 * (k & 1) + 1];
+                        b0 = ((l0 >> nsh) & 0x0f0f0f0fu) | (((v[6 * p + 4] >> hsh) & 0x03030303u) << 4);
+                        b1 = ((l1 >> nsh) & 0x0f0f0f0fu) | (((v[6 * p + 5] >> hsh) & 0x03030303u) << 4);
+                    }
+                    const uint2 x = *reinterpret_cast<const uint2 *>(xl(t) + 16 * group(s) + 8 * lh);
                     const v16i z = {};
                     return __builtin_amdgcn_mfma_i32_32x32x16_i8((long)((uint64_t)x.y << 32 | x.x),
                                                                  (long)((uint64_t)b1 << 32 | b0), z, 0, 0, 0);
                 };
                 v16i I = product(0);
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
+                for (int u = 0; u < 16 * NT; ++u) {
                     v16i next = I;
-                    if (t < 15) next = product(t + 1);     // in flight while this group's is used
-                    const int sc = scale6(group(t));
+                    if (u + 1 < 16 * NT) next = product(u + 1);            // in flight while this group's is used
+                    const int sc = scale6(group(u / NT)), t = u % NT;
 #pragma unroll
-                    for (int r = 0; r < 4 * FR; ++r) {
+                    for (int r = 0; r < 16; ++r) {
+                        if (16 * t + r >= 4 * FR) break;
                         const int e = I[r];
-                        V[r] = __mul24(sc, e) + V[r];
-                        asm volatile("" : "+v"(V[r]));
+                        V[16 * t + r] = __mul24(sc, e) + V[16 * t + r];
+                        asm volatile("" : "+v"(V[16 * t + r]));
                     }
                     __builtin_amdgcn_sched_barrier(0);
                     I = next;
@@ -216,11 +236,12 @@ struct SuperBlocks {
                 v8h bm;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) bm[e] = (_Float16)(32 * (lh ? scale6(8 + e) : scale6(e)));
-                mn = sums(xl, bm);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mn[t] = sums(xl(t), bm);
                 float dw = half_lo(v[28]);
                 asm volatile("" : "+v"(dw));
                 const float ndw = -dw;
-                fold([&](int r) { return fmaf(ndw, mn[r], (float)V[r] * dw); });
+                fold([&](int r) { return fmaf(ndw, mn[r / 16][r % 16], (float)V[r] * dw); });
             }
         }
         // acc += d8 * value of each of the tile's rows

@@ -672,14 +672,13 @@ __global__ __launch_bounds__(64 * WPG * G) void k_matmul_k_narrow(const uint8_t 
     matmul_k_body<F, SPLIT, true, G, WPG>(w, xq, y, M, N, ns, tiles_m);
 }
 
-// The experts' products of many rows: a tile of the plan and the weight rows of one
-// workgroup tile, consecutive workgroups on the same rows.  Bound as the prefill matmul
-// is; a compute unit holds one workgroup, so nothing covers the chain from the plan to
-// the first copy (Q2_K, 8192 rows of one expert of 4096 x 1536 126 us, the matmul 98;
-// 32768 rows of 64 experts of 1536 x 2048: Q2_K 258 us, 800 TOPS, Q4_K 345, 597, Q6_K
-// 565, 365).  Of A tiles without rows nothing is computed.  Eight tiles at a time, each
-// XCD on one, instead of a tile's columns in order: 2 to 5 % faster there, up to 6 %
-// slower with four experts; not kept.
+// The experts' products of many rows, Q6_K: a tile of the plan and the weight rows of
+// one workgroup tile, consecutive workgroups on the same rows.  Bound as the prefill
+// matmul is; a compute unit holds one workgroup, so nothing covers the chain from the
+// plan to the first copy (8192 rows of one expert of 4096 x 1536 270 us, the matmul 236;
+// 65536 rows of 64 experts of 1536 x 2048 1045 us, 395 TOPS, in tiles of 64 rows that
+// stream the weights 1112; Q2_K and Q4_K are faster in those).  Of A tiles without
+// rows nothing is computed.
 template <int F>
 __global__ __launch_bounds__(mk::NT) void k_experts_matmul_k(ExpertArgs a, int tiles_n) {
     constexpr int BN = mk::KW<F>::BN;
@@ -712,14 +711,7 @@ static hipError_t launch_experts(const ExpertArgs &a, hipStream_t st) {
     return hipLaunchKernel(k, dim3((unsigned)(grid_tiles(a) * tiles_n)), dim3(mk::NT), argv, (size_t)lds, st);
 }
 
-hipError_t launch_experts_k(int fmt, const ExpertArgs &a, hipStream_t st) {
-    switch (fmt) {
-        case F_Q2_K: return launch_experts<F_Q2_K>(a, st);
-        case F_Q4_K: return launch_experts<F_Q4_K>(a, st);
-        case F_Q6_K: return launch_experts<F_Q6_K>(a, st);
-    }
-    return hipErrorInvalidValue;
-}
+hipError_t launch_experts_q6_k(const ExpertArgs &a, hipStream_t st) { return launch_experts<F_Q6_K>(a, st); }
 
 // Largest super-block count whose tile offsets fit the 32-bit buffer offsets
 // (128 activation rows of ns * 292 bytes; 256 weight rows take fewer).

@@ -14,19 +14,22 @@ constexpr int64_t kMaxPairs = int64_t(1) << 26;
 // every workgroup of the product finds its rows from the ids by itself.
 constexpr int64_t kSelfPairs = kWave;
 
-// Rows of a tile: what one workgroup of a product takes of an expert's rows.  Short
-// tiles stream the weights (experts_stream.h), tiles of 128 rows are the prefill
-// matmul's.  Rows an expert, where they meet (us, 16 / 32 / 128 rows, 1536 x 2048):
-// 128 experts, 8 a token, Q4_0: 8 rows 54 / 56 / 147, 16 rows 68 / 69 / 147, 32 rows
-// 103 / 97 / 160, 64 rows 169 / 159 / 172, 128 rows - / 269 / 238; Q8_0: 64 rows 247 /
-// 209 / 184, 128 rows - / 345 / 255; Q4_K: 64 rows - / 125 / 153, 128 rows - / 211 / 226.
+// Rows of a tile of the plan: in what steps an expert's rows are cut, for products of
+// any format and width.  Tiles of 128 are what the prefill matmul's workgroups take, or
+// two of 64 or four of 32; all but those of 128 stream the weights (experts_stream.h).
+// us, 128 experts of 1536 x 2048, 8 a token, tiles of 16 / 32 / 64 / 128:
+//   rows an expert   25                     32                     64                    128
+//   Q4_0             90 / 86 / 96 / 127     105 / 99 / 108 / 133   - / 151 / 155 / 162   - / 263 / 256 / 231
+//   Q8_0             131 / 124 / 122 / 147  154 / 137 / 132 / 157  - / 207 / 187 / 185   - / 347 / 299 / 251
+//   Q5_1             156 / 136 / 139 / 175  180 / 155 / 157 / 180  - / 242 / 232 / 214   - / 426 / 390 / 305
+//   Q4_K             91 / 70 / 75 / 86      105 / 81 / 80 / 95     - / 125 / 118 / 150   - / 210 / 193 / 225
 // A few thousand pairs make too few workgroups of 128 rows (8 experts of 1024 x 1024,
-// 1400 pairs: 14.7 us in tiles of 32, 22 of 128).
-constexpr int kFewRows = 16, kNarrowRows = 32, kFullRows = 128;
+// 1400 pairs, Q4_0: 14.7 us in tiles of 32, 22 of 128).
+constexpr int kFewRows = 16, kNarrowRows = 32, kHalfRows = 64, kFullRows = 128;
 
 inline int tile_rows(int64_t pairs, int64_t experts) {
     const int64_t each = pairs / experts;
-    return each < 24 ? kFewRows : each < 96 || pairs < 4096 ? kNarrowRows : kFullRows;
+    return each < 20 ? kFewRows : each < 64 || pairs < 4096 ? kNarrowRows : kFullRows;
 }
 
 // Most tiles that `pairs` rows in experts + 1 groups (the last: pairs without
