@@ -16,7 +16,7 @@
 namespace qmm {
 
 constexpr int kFewWaves = 4;
-constexpr int kFewTiles = 32768;                       // of a launch: they lie along the grid's y, which holds 65535
+constexpr int kFewTiles = 32768;                       // of a launch at most: they lie along the grid's y, which holds 65535
 
 template <int BIT>
 __device__ __forceinline__ float sum_below(float v) {
@@ -114,9 +114,10 @@ static hipError_t launch_few(const ExpertArgs &a, hipStream_t st) {
     const int row_blocks = (a.N + RW * kFewWaves - 1) / (RW * kFewWaves);
     ExpertArgs args = a;
     const int tiles = (int)grid_tiles(a);
-    for (int tile0 = 0; tile0 < tiles; tile0 += kFewTiles) {
+    const int room = (1 << 23) / row_blocks, step = room < kFewTiles ? room : kFewTiles;       // 2^31 threads a launch
+    for (int tile0 = 0; tile0 < tiles; tile0 += step) {
         void *argv[] = {(void *)&args, (void *)&tile0, (void *)&xs, (void *)&ss};
-        const int y = tiles - tile0 < kFewTiles ? tiles - tile0 : kFewTiles;
+        const int y = tiles - tile0 < step ? tiles - tile0 : step;
         const hipError_t le = hipLaunchKernel(k, dim3((unsigned)row_blocks, (unsigned)y), dim3(64 * kFewWaves), argv, lds, st);
         if (le != hipSuccess) return le;
     }

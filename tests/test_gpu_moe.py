@@ -625,6 +625,22 @@ def test_plan_of_many_pairs(env, T, E, top, skew):
     assert np.array_equal(y.cpu().numpy(), np.repeat(want[..., None], 8, 2).astype(np.float32))
 
 
+def test_products_of_more_tiles_than_a_launch(env):
+    """K of one block and over 32768 tiles: several launches."""
+    torch, q, _ = env
+    T, E = 4_250_000, 2
+    _say("many tiles", T)
+    ids = np.random.default_rng(5).integers(-1, E, (T, 1)).astype(np.int32)
+    w, x, sums = _counted(torch, q, T, 1, E, K=32)
+    plan = q.experts_plan(T, 1, E)
+    y = torch.full((T, 1, 8), math.nan, device="cuda")
+    ids_d = _dev(torch, ids)
+    q.qmm_experts_plan(ids_d, E, plan)
+    q.qmm_experts_matmul_q8_0(w, x, ids_d, plan, y)
+    want = ((ids[:, 0] + 1) * sums).astype(np.float32)          # -1: zero
+    assert np.array_equal(y[:, 0].cpu().numpy(), np.repeat(want[:, None], 8, 1))
+
+
 @pytest.mark.parametrize("fmt,K", [("q4_0", 512), ("q8_0", 288), ("q5_1", 320), ("q4_1", 96), ("q2_k", 512), ("q6_k", 768)])
 @pytest.mark.parametrize("T", [1, 9, 60, 130, 700, 2300])
 def test_experts_other_rows_do_not_matter(env, fmt, K, T):
