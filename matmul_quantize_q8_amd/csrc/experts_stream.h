@@ -17,8 +17,8 @@
 //     registers at the start of a step and at once copies the next stage into it:
 //     a stage is on its way during all of a step, at half the LDS of two buffers,
 //     and three or four workgroups share a compute unit (128 experts of
-//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 26.5 us, 64 tokens 54.7 ->
-//     44.7; Q8_0, 64 tokens 117 -> 76, which is 4.8 TB/s of weights).  Only the activations, which the waves
+//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 25.0 us, 64 tokens 54.7 ->
+//     44.7; Q8_0, 64 tokens 117 -> 71.5, which is 5.1 TB/s of weights).  Only the activations, which the waves
 //     share, have two buffers.
 //   * Tiles of 16 rows where an expert has few: less LDS, less of the fold.
 //
@@ -243,13 +243,24 @@ inline int64_t stream_blocks(const ExpertArgs &a) {
 
 template <class C, int ROWS>
 static hipError_t pick_stream(const ExpertArgs &a, hipStream_t st) {
-    // The workgroup that suits the call's blocks (us, Q4_0 weights, one group of four
-    // waves / two of two / four of two):   40 blocks, 4 experts of 512 x 2048  17.1 / 10.8 / 8.9
-    //   114, 16 of 768 x 2048  11.3 / 9.0 / 8.5       128, 64 of 1024 x 2048  9.8 / 7.6 / 7.6
-    //   336, 8 of 3584 x 4096  33.0 / 24.8 / 29.3     448, 8 of 3500 x 4096  43.0 / 42.3 / 44.4
-    //   over 1000, 128 of 1536 x 2048  26.2 / 27.2 / 41.8 (16 tokens)  44.4 / 47.4 / 67.8 (64)
+    // The workgroup that suits the call's blocks of 128 weight rows.  Few: K cut over
+    // four groups of two waves, or two of two (us, Q4_0, one group of four waves / two
+    // of two / four of two):
+    //   40 blocks, 4 experts of 512 x 2048  17.1 / 10.8 / 8.9     114, 16 of 768 x 2048  11.3 / 9.0 / 8.5
+    //   128, 64 of 1024 x 2048  9.8 / 7.6 / 7.6                   336, 8 of 3584 x 4096  33.0 / 24.8 / 29.3
+    // Enough: one group, of two waves for the 32-value formats, whose smaller workgroups
+    // spread more evenly over the compute units; of four for the K-quants, whose
+    // activations are more bytes beside their weights, from 512 blocks on (one group of four
+    // waves / of two):
+    //   448 blocks, 8 of 3500 x 4096, 131 tokens  Q8_0 54 / 48  Q4_0 44 / 39  Q5_1 68 / 61  Q4_K 34 / 32  Q6_K 63 / 60
+    //   560, 8 of 3584 x 4096, 200 tokens         Q8_0 57 / 56  Q4_0 44 / 44  Q5_1 70 / 67  Q4_K 35 / 36  Q6_K 64 / 78
+    //   1900, 128 of 1536 x 2048, 500 tokens      Q8_0 135 / 131  Q4_0 93 / 96  Q5_1 152 / 146  Q4_K 78 / 87  Q6_K 141 / 146
     const int64_t blocks = stream_blocks(a);
-    if (blocks >= kEnoughBlocks) return launch_stream<C, ROWS, 1, 4>(a, st);
+    if (blocks >= kEnoughBlocks) {
+        if constexpr (C::BLOCKS == 1)
+            if (blocks >= 2 * kCUs) return launch_stream<C, ROWS, 1, 4>(a, st);
+        return launch_stream<C, ROWS, 1, 2>(a, st);
+    }
     if (blocks >= kFewBlocks) return launch_stream<C, ROWS, 2, 2>(a, st);
     return launch_stream<C, ROWS, 4, 2>(a, st);
 }
