@@ -16,15 +16,15 @@
 //   * A wave copies its own 32 weight rows into one LDS buffer, empties it into
 //     registers at the start of a step and at once copies the next stage into it:
 //     a stage is on its way during all of a step, at half the LDS of two buffers,
-//     and three or four workgroups share a compute unit (128 experts of
-//     1536 x 2048, 8 a token: Q4_0, 16 tokens 32.9 -> 25.0 us, 64 tokens 54.7 ->
-//     44.7; Q8_0, 64 tokens 117 -> 71.5, which is 5.1 TB/s of weights).  Only the activations, which the waves
-//     share, have two buffers.
+//     and several workgroups share a compute unit (128 experts of 1536 x 2048, 8 a
+//     token: Q4_0, 16 tokens 32.9 -> 25.0 us, 64 tokens 54.7 -> 44.7; Q8_0, 64 tokens
+//     117 -> 71.5, which is 5.1 TB/s of weights).  Only the activations, which the
+//     waves share, have two buffers.
 //   * Tiles of 16 rows where an expert has few: less LDS, less of the fold.
 //
 // A workgroup: a tile's rows x 32 WPG weight rows, wave w of a group alone on weight
-// rows 32 w .., one 32 x 32 MFMA tile a step of K (two, of rows 32 .. 63); G groups of WPG waves, each on
-// its part of K, which join in LDS in a fixed order.
+// rows 32 w .., one 32 x 32 MFMA tile a step of K (two, where there are rows 32 .. 63);
+// G groups of WPG waves, each on its part of K, which join in LDS in a fixed order.
 #pragma once
 
 #include <type_traits>

@@ -17,11 +17,12 @@ constexpr int64_t kSelfPairs = kWave;
 // Rows of a tile of the plan: in what steps an expert's rows are cut, for products of
 // any format and width.  Tiles of 128 are what the prefill matmul's workgroups take, or
 // two of 64 or four of 32; all but those of 128 stream the weights (experts_stream.h).
-// us, 128 experts of 1536 x 2048, 8 a token, tiles of 16 / 32 / 64 / 128:
+// us, 128 experts of 1536 x 2048, 8 a token, tiles of 16 / 32 / 64 / 128 (of 16, and of
+// 32 from 64 rows an expert on, in workgroups of four waves):
 //   rows an expert   25                     32                     64                    128
-//   Q4_0             90 / 86 / 96 / 127     105 / 99 / 108 / 133   - / 151 / 155 / 162   - / 263 / 256 / 231
-//   Q8_0             131 / 124 / 122 / 147  154 / 137 / 132 / 157  - / 207 / 187 / 185   - / 347 / 299 / 251
-//   Q5_1             156 / 136 / 139 / 175  180 / 155 / 157 / 180  - / 242 / 232 / 214   - / 426 / 390 / 305
+//   Q4_0             90 / 89 / 96 / 127     105 / 102 / 108 / 133  - / 151 / 155 / 162   - / 263 / 256 / 231
+//   Q8_0             131 / 119 / 122 / 147  154 / 130 / 132 / 157  - / 207 / 187 / 185   - / 347 / 299 / 251
+//   Q5_1             156 / 130 / 139 / 175  180 / 146 / 157 / 180  - / 242 / 232 / 214   - / 426 / 390 / 305
 //   Q4_K             91 / 70 / 75 / 86      105 / 81 / 80 / 95     - / 125 / 118 / 150   - / 210 / 193 / 225
 // A few thousand pairs make too few workgroups of 128 rows (8 experts of 1024 x 1024,
 // 1400 pairs, Q4_0: 14.7 us in tiles of 32, 22 of 128).
