@@ -18,6 +18,26 @@ __device__ __forceinline__ float activation(float g) {
     return g / (1.0f + expf(-z2));
 }
 
+// Gates below this have an activation of less than 2^-120, where e^-g and e^(-2z) overflow
+// soon and erfc falls below the normal values: activation() is 0 or coarse there while the
+// activation, and still more its product with `up`, is a number that f32 holds.
+template <int ACT> constexpr float kFarGate = ACT == G_SILU ? -88.0f : ACT == G_GELU ? -13.0f : -10.0f;
+
+// act(g) u there: g e^z u, z = g or the 2z above (1 + e^z rounds to 1), or with erfc's
+// scaled form g/2 erfcx(-g / sqrt 2) e^(-g^2 / 2) u; e^z in two halves around u, so that
+// neither is far below the normal values before the product is.
+template <int ACT>
+__device__ __forceinline__ float far_gated(float g, float u) {
+    float s = g, z = g;
+    if constexpr (ACT == G_GELU) {
+        s = 0.5f * g * erfcxf(-0.70710678118654752f * g);
+        z = -0.5f * g * g;
+    }
+    if constexpr (ACT == G_GELU_TANH) z = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    const float h = expf(0.5f * z);
+    return s * h * u * h;
+}
+
 constexpr int kGluThreads = 256;
 constexpr int64_t kGluGrid = 1 << 22;          // workgroups of a launch: a grid holds 2^32 threads
 
@@ -32,12 +52,20 @@ __global__ __launch_bounds__(kGluThreads) void k_glu(GluArgs a) {
         const int64_t row = row0 + at / (uint32_t)a.pieces;
         const int c = (int)(at % (uint32_t)a.pieces);
         if (row >= a.rows) continue;
-        float g[V], u[V];
+        float g[V], u[V], v[V], least = 0.0f;
         load_row<RT, V>(a.gate, row * a.gs + V * c, g);
         load_row<RT, V>(a.up, row * a.us + V * c, u);
 #pragma unroll
-        for (int k = 0; k < V; ++k) g[k] = activation<ACT>(g[k]) * u[k];
-        store_quantized<FMT, V>(a.xq + row * row_bytes, c, g);
+        for (int k = 0; k < V; ++k) {
+            v[k] = activation<ACT>(g[k]) * u[k];
+            least = fminf(least, g[k]);
+        }
+        if (least < kFarGate<ACT>) {                      // hardly ever
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (g[k] < kFarGate<ACT>) v[k] = far_gated<ACT>(g[k], u[k]);
+        }
+        store_quantized<FMT, V>(a.xq + row * row_bytes, c, v);
     }
 }
 

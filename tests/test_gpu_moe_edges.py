@@ -1,0 +1,40 @@
+"""Calls of the mixture-of-experts operators at the ends of what their contracts allow, on an MI355X."""
+import numpy as np
+import pytest
+
+import moe_ref as ref
+from test_gpu_moe import _dev, _say, env          # noqa: F401  (env: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# Gates for which e^-g, or the erfc of the GELU, leaves the normal f32 values while the activation does not (first
+# half), and where the activation itself is below them (second half), with factors that bring the products back.
+TAILS = {"silu": ((-92.0, -88.8, 1e37), (-103.0, -95.0, 3e38)),
+         "gelu": ((-13.3, -13.05, 1e38), (-14.2, -13.95, 3e38)),
+         "gelu_tanh": ((-10.2, -10.06, 1e37), (-10.6, -10.35, 3e38))}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", ["q8_0", "q8_k"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_glu_far_gates(env, act, fmt, dtype):
+    """The relative error r of a value is that of the whole range: 16 f32 steps times the 104 that a far gate's
+    exponent, rounded to 2^-24 of itself, can amplify one by; the blocks then as at any other gate."""
+    torch, q, _ = env
+    _say("glu far", act, fmt, dtype)
+    V = ref.VALUES[fmt]
+    g, u = np.empty((2, V), np.float32), np.empty((2, V), np.float32)
+    for i, (lo, hi, factor) in enumerate(TAILS[act]):
+        g[i], u[i] = np.linspace(lo, hi, V), factor * np.where(np.arange(V) % 3, 1, -1)
+    gate, up = _dev(torch, g, dtype), _dev(torch, u, dtype)
+    xq = torch.zeros(2, q.row_bytes(fmt, V), dtype=torch.uint8, device="cuda")
+    q.GLU[fmt](gate, up, xq, act=act)
+    want = ref.activation(gate.float().cpu().numpy(), act) * up.double().cpu().numpy()
+    values, d = ref.decoded(xq.cpu().numpy(), fmt)
+    r = 16 * 104 * 2.0 ** -24
+    amax = np.abs(want).max(1)
+    assert np.all(amax > 1e-5)
+    step, tiny = (2.0 ** -11, 2.0 ** -25) if fmt == "q8_0" else (2.0 ** -23, 0)
+    assert np.all(np.abs(d[:, 0] - amax / 127) <= (step + 2 * r) * amax / 127 + tiny)
+    assert np.all(np.abs(values - want) <= (amax / 127 * (0.5 + 127 * (step + 2 * r)) + 127 * tiny)[:, None])
