@@ -558,8 +558,8 @@ qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *
  * One serves every product with these ids.
  *   ids  : int32 [T][top_k], device.
  *   plan : device, 16-byte aligned, qmm_experts_plan_bytes(T, top_k, E) bytes (0:
- *          sizes outside the limits), written.  Plans that are in use at the same
- *          time need a buffer each.
+ *          sizes outside the limits) or more, written; a size suffices for fewer
+ *          tokens too.  Plans that are in use at the same time need a buffer each.
  * Calls of up to 64 pairs launch nothing: their products read the ids. */
 int64_t qmm_experts_plan_bytes(int64_t T, int64_t top_k, int64_t E);
 qmm_status qmm_experts_plan(const int32_t *ids, void *plan, int64_t plan_bytes, int64_t T, int64_t top_k, int64_t E,

@@ -65,10 +65,12 @@ struct Plan {
     const int *pair, *token, *counts;
 };
 
+// Never less for more pairs, so that a buffer serves smaller calls too: room for the counts of 256
+// segments wherever segments get longer (their number then falls where pairs grow).
 inline int64_t plan_bytes(int64_t pairs, int64_t experts) {
     const int rows = tile_rows(pairs, experts);
-    const int64_t segments = plan_segments(pairs);
-    return max_tiles(pairs, experts, rows) * (8 + 8 * rows) + (segments > 1 ? segments * (experts + 1) * 4 : 0);
+    const int64_t most = (pairs + 1023) / 1024, segments = most < 256 ? most : 256;
+    return max_tiles(pairs, experts, rows) * (8 + 8 * rows) + (plan_segments(pairs) > 1 ? segments * (experts + 1) * 4 : 0);
 }
 
 inline Plan plan_at(const void *plan, int64_t pairs, int64_t experts) {

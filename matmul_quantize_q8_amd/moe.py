@@ -144,12 +144,12 @@ def qmm_route(logits, ids, weights, score: str = "softmax", bias=None, groups: i
 
 # -- experts ---------------------------------------------------------------------------
 def qmm_experts_plan_bytes(T: int, top_k: int, E: int) -> int:
-    """Bytes of the plan of T tokens with top_k of E experts (0 for sizes outside the limits)."""
+    """Bytes of the plan of up to T tokens with top_k of E experts (0 for sizes outside the limits)."""
     return _lib().qmm_experts_plan_bytes(T, top_k, E)
 
 
 def experts_plan(T: int, top_k: int, E: int, device="cuda"):
-    """A new buffer for qmm_experts_plan."""
+    """A new buffer for qmm_experts_plan, for up to T tokens."""
     size = qmm_experts_plan_bytes(T, top_k, E)
     if size == 0:
         raise ValueError(f"no plan of {T} tokens with {top_k} of {E} experts")

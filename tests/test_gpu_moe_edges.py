@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import moe_ref as ref
-from test_gpu_moe import _dev, _say, env          # noqa: F401  (env: the fixture)
+from test_gpu_moe import _counted, _dev, _say, env          # noqa: F401  (env: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,20 @@ def test_glu_far_gates(env, act, fmt, dtype):
     step, tiny = (2.0 ** -11, 2.0 ** -25) if fmt == "q8_0" else (2.0 ** -23, 0)
     assert np.all(np.abs(d[:, 0] - amax / 127) <= (step + 2 * r) * amax / 127 + tiny)
     assert np.all(np.abs(values - want) <= (amax / 127 * (0.5 + 127 * (step + 2 * r)) + 127 * tiny)[:, None])
+
+
+def test_one_plan_buffer_for_every_batch(env):
+    """A buffer made for the largest batch, used by smaller ones in turn: exact products of whole numbers."""
+    torch, q, _ = env
+    top, E, most = 4, 64, (1 << 16) + 1
+    plan = q.experts_plan(most, top, E)
+    for T in (most, most - 1, 3, 700, 20, 16384):
+        _say("plan buffer", T)
+        ids = np.random.default_rng(T).integers(-1, E, (T, top)).astype(np.int32)
+        w, x, sums = _counted(torch, q, T, top, E)
+        y = torch.full((T, top, 8), float("nan"), device="cuda")
+        ids_d = _dev(torch, ids)
+        q.qmm_experts_plan(ids_d, E, plan)
+        q.qmm_experts_matmul_q8_0(w, x, ids_d, plan, y)
+        want = ((ids + 1) * sums[:, None]).astype(np.float32)              # -1: zero
+        assert np.array_equal(y.cpu().numpy(), np.repeat(want[..., None], 8, 2))

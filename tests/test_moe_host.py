@@ -87,6 +87,20 @@ def test_plan_bytes(q):
     assert size(1 << 26, 1, 8) > 0 and size(1 << 20, 64, 512) > 0
 
 
+@pytest.mark.parametrize("top,E", [(1, 1), (1, 8), (1, 512), (2, 8), (4, 512), (8, 128), (64, 64)])
+def test_plan_bytes_suffice_for_fewer_tokens(q, top, E):
+    """A buffer made for the largest batch serves every smaller one: around each change of the rows of a tile and of
+    the pairs of a segment, and between."""
+    size = q.qmm_experts_plan_bytes
+    edges = {n // top + d for n in (1, 64, 2048, 4096, 16 * E, 20 * E, 32 * E, 64 * E, 128 * E, 1 << 18, 1 << 26) for d in
+             range(-70, 71)}
+    between = {int(1.003 ** k) for k in range(6100)} | {(1 << 18) * k // (16 * top) for k in range(1, 64)}
+    sizes = [size(T, top, E) for T in sorted(edges | between) if 1 <= T <= (1 << 26) // top]
+    assert len(sizes) > 2000 and sizes == sorted(sizes) and sizes[0] > 0
+    # the calls take it
+    assert plan(q, T=(1 << 18) // top, top=top, E=E, bytes=size((1 << 18) // top + 1, top, E)) == NULL
+
+
 def plan(q, **kw):
     a = dict(ids=A, plan=None, bytes=1 << 20, T=100, top=2, E=8)
     a.update(kw)
