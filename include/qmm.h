@@ -545,7 +545,7 @@ qmm_status qmm_glu_q8_k(const void *gate, const void *up, void *xq8k, int dtype,
  * logit shows in the weights.  Scores are f64, so the order is the formula's; without
  * a bias it is the logits' own.
  *   logits  : [T][E] in dtype, row t at t * logits_stride elements; any alignment
- *             and stride >= 0.
+ *             and stride >= 0 (one row: its stride is not read).  T < 2^24.
  *   bias    : f32 [E], or NULL.
  *   ids     : int32 [T][top_k], written.    weights : f32 [T][top_k], written.
  * top_k <= groups_kept * E/groups; groups <= 64; scale finite. */

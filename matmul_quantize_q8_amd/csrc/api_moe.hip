@@ -156,7 +156,7 @@ qmm_status qmm_route(const void *logits, int dtype, const float *bias, int32_t *
     if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID) return QMM_E_SHAPE;
     if (groups < 1 || groups > kWave || E % groups != 0 || groups_kept < 1 || groups_kept > groups) return QMM_E_SHAPE;
     if (top_k > E / groups * groups_kept || (group_top != 1 && group_top != 2) || !std::isfinite(scale)) return QMM_E_SHAPE;
-    if (logits_stride < 0 || logits_stride > kMaxBytes || (__int128)(T - 1) * logits_stride + E > kMaxBytes / 4)
+    if (T > 1 && (logits_stride < 0 || logits_stride > kMaxBytes || (__int128)(T - 1) * logits_stride + E > kMaxBytes / 4))
         return QMM_E_SHAPE;
     QMM_TRY(check_index(logits, row_type_bytes(dtype)));
     QMM_TRY(check_index(ids, 4));
@@ -208,9 +208,11 @@ qmm_status qmm_experts_combine(const float *y, const float *weights, const void 
         if (residual != nullptr) QMM_TRY(check_in(residual, dtype, T, N, residual_stride));
         QMM_TRY(check_written(out, dtype, T, N, out_stride));
     } else {                                               // value by value: any stride will do
-        for (const int64_t s : {residual != nullptr ? residual_stride : 0, out_stride})
-            if (s < 0 || s > kMaxBytes / 4 / T) return QMM_E_SHAPE;
-        if (T > 1 && out_stride < N) return QMM_E_SHAPE;
+        if (T > 1) {
+            for (const int64_t s : {residual != nullptr ? residual_stride : 0, out_stride})
+                if (s < 0 || s > kMaxBytes / 4 / T) return QMM_E_SHAPE;
+            if (out_stride < N) return QMM_E_SHAPE;
+        }
         QMM_TRY(check_index(out, row_type_bytes(dtype)));
         if (residual != nullptr) QMM_TRY(check_index(residual, row_type_bytes(dtype)));
     }

@@ -55,3 +55,15 @@ def test_one_plan_buffer_for_every_batch(env):
         q.qmm_experts_matmul_q8_0(w, x, ids_d, plan, y)
         want = ((ids + 1) * sums[:, None]).astype(np.float32)              # -1: zero
         assert np.array_equal(y.cpu().numpy(), np.repeat(want[..., None], 8, 2))
+
+
+@pytest.mark.parametrize("N", [7, 8])
+def test_combine_of_one_row_of_any_stride(env, N):
+    """A row's stride that no size could hold is not read."""
+    torch, q, _ = env
+    _say("combine one row", N)
+    y, w, r = torch.randn(1, 3, N, device="cuda"), torch.rand(1, 3, device="cuda"), torch.randn(1, N, device="cuda")
+    out, far = torch.empty(1, N, device="cuda"), torch.empty(N, device="cuda").as_strided((1, N), (1 << 60, 1))
+    q.qmm_experts_combine(y, w, out, residual=r)
+    q.qmm_experts_combine(y, w, far, residual=r.as_strided((1, N), (1 << 60, 1)))
+    assert torch.equal(out, far) and torch.isfinite(out).all()

@@ -156,6 +156,21 @@ def test_combine(q, kw, code):
     assert combine(q, **kw) == code
 
 
+@pytest.mark.parametrize("kw", [dict(os=-3), dict(os=1), dict(rs=-1), dict(rs=1 << 62, os=1 << 62), dict(os=1 << 50)])
+def test_combine_of_one_row_reads_no_stride(q, kw):
+    """Rows of N values, a multiple of four or not; two rows are refused."""
+    for N in (63, 64):
+        a = dict(dict(N=N, rs=N, os=N, T=1), **kw)
+        assert combine(q, **a) == NULL, N
+        assert combine(q, **dict(a, T=2)) != NULL, N
+
+
+@pytest.mark.parametrize("stride", [-1, 1, 1 << 62])
+def test_route_of_one_row_reads_no_stride(q, stride):
+    assert route(q, T=1, stride=stride) == NULL
+    assert route(q, T=2, stride=stride) == (NULL if stride == 1 else SHAPE)
+
+
 def test_binding_refuses_other_tensors(q):
     """Shapes, types and devices are checked before the library is called."""
     import torch
