@@ -182,7 +182,7 @@ def _experts_matmul(fmt):
         rows = xq.shape[0]
         shape = (T, top, N) if len(y.shape) == 3 else (T * top, N)
         bytes_ = plan.numel()
-        _call(name, w.data_ptr(), expert if E > 1 else max(expert, (N * rb + 15) // 16 * 16),
+        _call(name, w.data_ptr(), expert if E > 1 else (N * rb + 15) // 16 * 16,       # one expert: any stride
               _array("xq", xq, torch.uint8, (rows, _blocks(act, K)), device), rows,
               _array("ids", ids, torch.int32, (T, top), device), _array("plan", plan, torch.uint8, (bytes_,), device),
               bytes_, _array("y", y, torch.float32, shape, device), T, top, E, N, K, _stream(stream, device))

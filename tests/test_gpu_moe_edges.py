@@ -67,3 +67,19 @@ def test_combine_of_one_row_of_any_stride(env, N):
     q.qmm_experts_combine(y, w, out, residual=r)
     q.qmm_experts_combine(y, w, far, residual=r.as_strided((1, N), (1 << 60, 1)))
     assert torch.equal(out, far) and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_experts_of_one_matrix_of_any_stride(env, T):
+    """One expert's matrix, a view of rows of matrices that lie at no whole 16 bytes."""
+    torch, q, _ = env
+    _say("one matrix", T)
+    w, x, sums = _counted(torch, q, T, 1, 3, N=9, K=64)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    plan = q.experts_plan(T, 1, 1)
+    q.qmm_experts_plan(ids, 1, plan)
+    for one in (w[:1, :7], w[0, :7].as_strided((1, 7, 68), (1 << 60, 68, 1))):
+        assert one.stride(0) % 16 != 0 or one.stride(0) == 1 << 60
+        y = torch.full((T, 1, 7), float("nan"), device="cuda")
+        q.qmm_experts_matmul_q8_0(one, x, ids, plan, y)
+        assert np.array_equal(y.cpu().numpy()[:, 0], np.repeat(sums[:, None], 7, 1).astype(np.float32))
