@@ -122,8 +122,9 @@ qmm_status experts_matmul(int fmt, few_launch few, const void *w, int64_t stride
     // values is no stage of any other
     if (T == 1 || (!k && nb < 2)) return launched(few(a, st));
     // Q6_K, 64 experts of 1536 x 2048 with 192 / 256 / 512 / 1024 rows each, in tiles of 64 249 / 314 / 580 / 1112 us, of 128
-    // 263 / 325 / 567 / 1045
-    if (fmt == F_Q6_K && pairs / E >= 384 && !in_parts(a)) return launched(launch_experts_q6_k(a, st));
+    // 263 / 325 / 567 / 1045; of a plan in steps of 32, most of those would be empty (8 experts of 4096 x 2048, 500 rows each
+    // 433 us, streamed 234; 4 of 1048 x 2048 81 / 53)
+    if (fmt == F_Q6_K && a.rows == kFullRows && pairs / E >= 384 && !in_parts(a)) return launched(launch_experts_q6_k(a, st));
     if (k) return launched(launch_experts_stream_k(fmt, a, st));
     const bool stages = (a.rows < kFullRows || in_parts(a)) && experts_stream_32_suits(fmt, a);
     return launched(stages ? launch_experts_stream_32(fmt, a, st) : launch_experts_32(fmt, a, st));

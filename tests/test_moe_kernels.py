@@ -64,6 +64,8 @@ def _cases():
                                               (64, "1, 4", 2100, 2, 16, 904)):         # and of 64
             for K in (768, 1024) if rows == 64 else (768, 1280):
                 yield f"k_experts_stream<qmm::SuperBlocks<{c}>, {rows}, {workgroup}>", fmt, T, top, E, N, K, K == 768
+        # many rows an expert, and so few pairs that the plan's tiles have 32
+        yield f"k_experts_stream<qmm::SuperBlocks<{c}>, 32, 1, 4>", fmt, 1000, 2, 4, 1048, 768, False
     for K in (768, 1024):
         yield "k_experts_matmul_k<4>", "q6_k", 1700, 3, 8, 400, K, K == 768
 
