@@ -44,19 +44,19 @@ struct Blocks32 {
         int lane, lh;
         uint32_t up;                                       // the nibbles that the lane half feeds, into the high halves
         uint32_t hi_nibbles = 0xF0F0F0F0u, sign = 0x80808080u;
-        int wodd = 0, xodd = 0, xlead = 0;                 // ODD: rows' numbers odd (xodd: bit i of row 8i + lane / 8; xlead: bit t)
+        int wodd = 0, xodd = 0, xlead = 0;                 // ODD: rows' numbers odd (xodd: bit i of row 8i + lane / 8)
         v16i bias;
         static constexpr int NV = Q8 ? 36 : WBYTES / 4;
         uint32_t v[NV];
-        static constexpr int NT = FR > 4 ? 2 : 1;          // MFMA tiles of 32 rows
-        float acc[16 * NT];
+        static_assert(ROWS <= 32 && FR <= 4, "one MFMA tile of 32 rows");
+        float acc[16];
 
         __device__ __forceinline__ Step(const uint8_t *w, uint8_t *own, int l)
             : ws(w), dxw(reinterpret_cast<float *>(own)), lane(l), lh(l >> 5), up(lh ? 0u : 4u) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) bias[r] = 0x4B400000;
 #pragma unroll
-            for (int r = 0; r < 16 * NT; ++r) acc[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
             asm volatile("" : "+v"(bias));                 // in vector registers for the whole loop
             asm volatile("" : "+v"(hi_nibbles), "+v"(sign));
         }
@@ -66,8 +66,7 @@ struct Blocks32 {
             wodd = n & 1;
 #pragma unroll
             for (int i = 0; i < FR; ++i) xodd |= (src[min(8 * i + (lane >> 3), M - 1)] & 1) << i;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) xlead |= (src[min((lane & (ROWS < 32 ? ROWS - 1 : 31)) + 32 * t, M - 1)] & 1) << t;
+            xlead = src[min(lane & (ROWS - 1), M - 1)] & 1;
         }
         // the 16 codes of block b of a Q8_0 row that the lane's half feeds: the dwords that hold them, and out of these;
         // lead: the bytes before the row's stage (0 or 2, ODD only)
@@ -154,9 +153,9 @@ struct Blocks32 {
         }
         // first: the stage's first block; skip: blocks of it that were in the stage before
         __device__ __forceinline__ void work(const uint8_t *xs, int first, int skip) {
-            const int xrow = lane & (ROWS < 32 ? ROWS - 1 : 31);                 // rows past the tile's LDS rows repeat them
-            auto xl = [&](int t) { return xs + 16 * XC * (xrow + 32 * t); };     // of MFMA tile t
-            auto lead = [&](int t) { return ODD ? 2 * (((xlead >> t) + first) & 1) : 0; };
+            const int xrow = lane & (ROWS - 1);                                  // rows past the tile's LDS rows repeat them
+            const uint8_t *const xl = xs + 16 * XC * xrow;
+            const int lead = ODD ? 2 * ((xlead + first) & 1) : 0;
             // the wave's dx as f32: lane l takes block l % 8 of rows l / 8, l / 8 + 8, ..
 #pragma unroll
             for (int i = 0; i < FR; ++i) {
@@ -176,50 +175,42 @@ struct Blocks32 {
                     dxw[8 * ROWS + ROWS * b + row] = TAIL && b < skip ? 0.0f : d * (float)sum;
                 }
             }
-            // Steps u = (block, MFMA tile).  Rows' codes are read two steps ahead of their fold and dx one step ahead, and
-            // the next step's product is under way while one is folded: a wave that is alone on its SIMD waits for none of
-            // them.
+            // Rows' codes are read two blocks ahead of their fold and dx one block ahead, and the next block's product is
+            // under way while one is folded: a wave that is alone on its SIMD waits for none of them.
             struct Dx { float4 x[4]; };
-            auto dx = [&](int b, int t) {
+            auto dx = [&](int b) {
                 Dx q;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * t + i < FR)
-                        q.x[i] = *reinterpret_cast<const float4 *>(dxw + ROWS * b + 32 * t + 8 * i + 4 * lh);
+                for (int i = 0; i < FR; ++i) q.x[i] = *reinterpret_cast<const float4 *>(dxw + ROWS * b + 8 * i + 4 * lh);
                 return q;
             };
-            Raw raw = raw16(xl(0), 0, lead(0));
-            v4i x = codes16(raw, 0, lead(0)), w = operand(0);
+            Raw raw = raw16(xl, 0, lead);
+            v4i x = codes16(raw, 0, lead), w = operand(0);
             v16i d = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, w, bias, 0, 0, 0);
-            raw = raw16(xl(1 % NT), 1 / NT, lead(1 % NT));
-            Dx x0 = dx(0, 0), x1 = x0;
-            float dw = 0.0f, nb = 0.0f;
+            raw = raw16(xl, 1, lead);
+            Dx x0 = dx(0), x1 = x0;
 #pragma unroll
-            for (int u = 0; u < 8 * NT; ++u) {
-                const int b = u / NT, t = u % NT;
+            for (int b = 0; b < 8; ++b) {
                 v16i next = bias;
-                if (u + 1 < 8 * NT) {
-                    const int b1 = (u + 1) / NT, t1 = (u + 1) % NT;
-                    x = codes16(raw, b1, lead(t1));
-                    if (u + 2 < 8 * NT) raw = raw16(xl((u + 2) % NT), (u + 2) / NT, lead((u + 2) % NT));
-                    x1 = dx(b1, t1);
-                    if (t1 == 0) w = operand(b1);
+                if (b + 1 < 8) {
+                    x = codes16(raw, b + 1, lead);
+                    if (b + 2 < 8) raw = raw16(xl, b + 2, lead);
+                    x1 = dx(b + 1);
+                    w = operand(b + 1);
                     next = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, w, bias, 0, 0, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (t == 0) dw = scale(b), nb = dw * -es::kBias;
+                const float dw = scale(b), nb = dw * -es::kBias;
                 float v0[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    if (16 * t + r >= 4 * FR) break;
+                for (int r = 0; r < 4 * FR; ++r) {
                     const int e = d[r];
                     v0[r] = fmaf(__int_as_float(e), dw, nb);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (4 * t + i >= FR) break;
+                for (int i = 0; i < FR; ++i) {
                     const float4 q = x0.x[i];
-                    float *a = acc + 16 * t + 4 * i;
+                    float *a = acc + 4 * i;
                     a[0] = fmaf(v0[4 * i], q.x, a[0]);
                     a[1] = fmaf(v0[4 * i + 1], q.y, a[1]);
                     a[2] = fmaf(v0[4 * i + 2], q.z, a[2]);
@@ -235,11 +226,11 @@ struct Blocks32 {
                         const float c = fmaf(f16_bits_to_f32(dm), 128.0f, f16_bits_to_f32(dm >> 16) * (1.0f / OUT_SCALE));
                         v16f s;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = acc[16 * t + r];
-                        const float m = dxw[8 * ROWS + ROWS * (b - 1 + lh) + xrow + 32 * t];
+                        for (int r = 0; r < 16; ++r) s[r] = acc[r];
+                        const float m = dxw[8 * ROWS + ROWS * (b - 1 + lh) + xrow];
                         s = __builtin_amdgcn_mfma_f32_32x32x2f32(m, c, s, 0, 0, 0);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[16 * t + r] = s[r];
+                        for (int r = 0; r < 16; ++r) acc[r] = s[r];
                     }
                 }
             }

@@ -582,11 +582,8 @@ __device__ __forceinline__ void matmul_k_body(const uint8_t *__restrict__ w, con
         if (live == TI) {
             compute_tiles(sb, std::integral_constant<int, TI>());
         } else if constexpr (GROUPED) {
+            static_assert(TI == 2, "Q6_K: a wave has two A tiles");
             if (live == 1) compute_tiles(sb, std::integral_constant<int, 1>());
-            if constexpr (TI == 4) {
-                if (live == 2) compute_tiles(sb, std::integral_constant<int, 2>());
-                if (live == 3) compute_tiles(sb, std::integral_constant<int, 3>());
-            }
         }
     };
 
