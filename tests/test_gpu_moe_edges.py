@@ -83,3 +83,66 @@ def test_experts_of_one_matrix_of_any_stride(env, T):
         y = torch.full((T, 1, 7), float("nan"), device="cuda")
         q.qmm_experts_matmul_q8_0(one, x, ids, plan, y)
         assert np.array_equal(y.cpu().numpy()[:, 0], np.repeat(sums[:, None], 7, 1).astype(np.float32))
+
+
+def _ones(torch, fmt, E, N, blocks):
+    """Matrices of codes that stand for 1, expert e's scale 2^(e % 3): [E][N][row bytes]."""
+    scale = {e: [int(b) for b in np.float16(2.0 ** e).reshape(1).view(np.uint8)] for e in range(3)}
+    block = {"q8_0": lambda d: d + [1] * 32, "q4_0": lambda d: d + [0x99] * 16,
+             "q4_k": lambda d: d + [0, 0] + [1] * 4 + [0] * 4 + [1] * 4 + [0x11] * 128,          # scales 1, minima 0
+             "q6_k": lambda d: [0x11] * 128 + [0xaa] * 64 + [1] * 16 + d}[fmt]                   # 33 - 32
+    three = torch.tensor([block(scale[e]) for e in range(3)], dtype=torch.uint8, device="cuda")
+    row = three.repeat(1, blocks)[torch.arange(E, device="cuda") % 3]
+    return row[:, None].expand(E, N, row.shape[1]).contiguous()
+
+
+def _signs(torch, fmt, T, blocks):
+    """Rows of -1, 0 and 1 with scale 1, and their sums."""
+    values = 256 if fmt.endswith("_k") else 32
+    codes = torch.randint(-1, 2, (T, blocks, values), dtype=torch.int8, device="cuda")
+    if values == 32:
+        x = torch.empty(T, blocks, 34, dtype=torch.uint8, device="cuda")
+        x[..., 0], x[..., 1] = 0, 0x3c
+        x[..., 2:] = codes.view(torch.uint8)
+    else:
+        x = torch.empty(T, blocks, 292, dtype=torch.uint8, device="cuda")
+        x[..., :4] = torch.tensor([0, 0, 0x80, 0x3f], dtype=torch.uint8, device="cuda")
+        x[..., 4:260] = codes.view(torch.uint8)
+        x[..., 260:] = codes.view(T, blocks, 16, 16).sum(-1, dtype=torch.int16).view(torch.uint8).view(T, blocks, 32)
+    return x.view(T, -1), codes.sum((1, 2), dtype=torch.int64)
+
+
+@pytest.mark.parametrize("fmt,T,E,N,blocks", [
+    ("q8_0", 3855, 240, 8, 32768), ("q4_0", 3855, 240, 8, 32767), ("q8_0", 3855, 100, 8, 32768),     # tiles of 16, of 32
+    ("q8_0", 3854, 20, 8, 32774), ("q4_0", 4200, 1, 520, 30070),                          # the prefill tiles of 32 and 128
+    ("q6_k", 3855, 240, 8, 3815), ("q4_k", 4200, 1, 700, 3501), ("q6_k", 4200, 1, 700, 3501)])       # of 16, 64, 128
+def test_experts_of_nearly_4_gib_of_rows(env, fmt, T, E, N, blocks):
+    """Rows whose offsets pass 2^31 and end just below 2^32 bytes: exact products of whole numbers."""
+    torch, q, _ = env
+    _say("4 GiB", fmt, T, E, N, blocks)
+    w = _ones(torch, fmt, E, N, blocks)
+    x, sums = _signs(torch, fmt, T, blocks)
+    assert 0.99 * 2 ** 32 < x.numel() < 2 ** 32
+    ids = torch.randint(0, E, (T, 1), dtype=torch.int32, device="cuda")
+    plan, y = q.experts_plan(T, 1, E), torch.full((T, 1, N), float("nan"), device="cuda")
+    q.qmm_experts_plan(ids, E, plan)
+    q.EXPERTS_MATMUL[fmt](w, x, ids, plan, y)
+    want = (sums * 2 ** (ids[:, 0] % 3)).float()
+    assert torch.equal(y[:, 0], want[:, None].expand(T, N))
+
+
+def test_norm_of_more_rows_than_a_grid(env):
+    """Workgroups that take a second row, against the same rows in calls of fewer."""
+    torch, q, _ = env
+    T, K = (1 << 20) + 77, 64
+    _say("norm of many rows", T)
+    x, r = torch.randn(T, K, device="cuda"), torch.randn(T, K, device="cuda")
+    xq, s, y = torch.zeros(T, 68, dtype=torch.uint8, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    q.qmm_rms_norm_q8_0(x, None, xq, residual=r, sum=s, y=y)
+    for part in (slice(0, 1000), slice((1 << 20) - 500, T)):
+        n = len(range(*part.indices(T)))
+        xq2, s2, y2 = torch.empty(n, 68, dtype=torch.uint8, device="cuda"), x.new_empty(n, K), x.new_empty(n, K)
+        q.qmm_rms_norm_q8_0(x[part], None, xq2, residual=r[part], sum=s2, y=y2)
+        assert torch.equal(xq[part], xq2) and torch.equal(s[part], s2) and torch.equal(y[part], y2)
+    want = ref.norm((x[-77:] + r[-77:]).cpu().numpy(), None, 1e-6)
+    assert np.all(np.abs(y[-77:].cpu().numpy() - want) <= (2.0 ** -24 + 1e-12) * np.abs(want) + 2.0 ** -149)
