@@ -1,5 +1,6 @@
 #pragma once
-// Products of one row, or a few, with an expert's weights: y[p] = W[id_p] x[p].
+// Products of one token with its experts' weights, y[p] = W[id_p] x[p], and of any number
+// of tokens with rows of one block of 32 values, which are no stage of the other kernels.
 //
 // Bound by the weight stream, as a decode step is: a token's experts are read once
 // from HBM.  A workgroup takes a tile of an expert's rows (of one token nearly

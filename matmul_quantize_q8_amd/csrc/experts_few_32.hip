@@ -1,4 +1,4 @@
-// Experts' products of a few rows: Q4_0, Q8_0 weights (kernel: experts_few.h).
+// Experts' products of one token: Q4_0, Q8_0 weights (kernel: experts_few.h).
 #include "experts_few.h"
 
 namespace qmm {

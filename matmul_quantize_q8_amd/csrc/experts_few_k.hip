@@ -1,4 +1,4 @@
-// Experts' products of a few rows: Q2_K, Q4_K, Q6_K weights (kernel: experts_few.h).
+// Experts' products of one token: Q2_K, Q4_K, Q6_K weights (kernel: experts_few.h).
 #include "experts_few.h"
 
 namespace qmm {

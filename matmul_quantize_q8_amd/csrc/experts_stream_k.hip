@@ -1,4 +1,4 @@
-// Experts' products of up to 32 rows a tile, K-quant weight formats.
+// Experts' products of up to 64 rows a tile, K-quant weight formats.
 //
 // A stage is one super-block; the products are those of the K-quant prefill:
 //   Q2_K  d8 (d V - dmin Mn), V = sum sc I on int8 MFMA with the group scales folded

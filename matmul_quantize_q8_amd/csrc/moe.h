@@ -24,8 +24,12 @@ constexpr int64_t kSelfPairs = kWave;
 //   Q8_0             131 / 119 / 122 / 147  154 / 130 / 132 / 157  - / 207 / 187 / 185   - / 347 / 299 / 251
 //   Q5_1             156 / 130 / 139 / 175  180 / 146 / 157 / 180  - / 242 / 232 / 214   - / 426 / 390 / 305
 //   Q4_K             91 / 70 / 75 / 86      105 / 81 / 80 / 95     - / 125 / 118 / 150   - / 210 / 193 / 225
-// A few thousand pairs make too few workgroups of 128 rows (8 experts of 1024 x 1024,
-// 1400 pairs, Q4_0: 14.7 us in tiles of 32, 22 of 128).
+// Below 4096 pairs the rule stays with 32: whole workgroups of 128 rows were too few there
+// (8 experts of 1024 x 1024, 1400 pairs, Q4_0: 14.7 us in tiles of 32, 22 of 128).  Products
+// have come to take a step of 128 in parts where columns are few, and with that steps of 128
+// are the faster ones at 128 rows an expert and more, most of all of wide experts (2 of 8, in
+// steps of 32 / 128, Q4_0, Q8_0, Q4_K, Q6_K: of 1024 x 1024, 1536 tokens 25 / 23, 30 / 23, 18 / 16,
+// 33 / 26; of 14336 x 4096, 1024 tokens 546 / 399, 706 / 446, 415 / 360, 780 / 659).
 constexpr int kFewRows = 16, kNarrowRows = 32, kHalfRows = 64, kFullRows = 128;
 
 inline int tile_rows(int64_t pairs, int64_t experts) {
